@@ -182,6 +182,43 @@ int pkv_free_list(const pkv_pool* pool, int32_t* out, int64_t* n);
 int pkv_append_kv(const pkv_pool* pool, int32_t layer, const void* k_new, const void* v_new,
                   const int32_t* slot_mapping, int32_t n_tok, void* k_pool, void* v_pool, pkv_stream_t stream);
 
+/* Rotary positions: what turns a position into the rotation of a head's element pairs.
+ * Frequency i < rotary_dim / 2 rotates one pair (x1, x2) of every query and key head by the
+ * angle w = p * inv_freq[i], p the token's position on the axis that the frequency belongs to:
+ *   (x1, x2) -> (x1 cos w - x2 sin w, x2 cos w + x1 sin w).
+ * One axis is the position in the text; several (time, height, width of an image's or a
+ * video's patches) each have frequencies of their own. */
+typedef struct pkv_rotary {
+  const float* inv_freq; /* device float32 [rotary_dim / 2], finite */
+  int32_t rotary_dim;    /* elements of a head that are rotated: even, 2 .. d_head; the rest pass */
+  int32_t interleaved;   /* 0: pair i is elements (i, i + rotary_dim / 2); 1: elements (2i, 2i + 1) */
+  int32_t n_axes;        /* position axes, 1 .. 4 */
+  uint8_t axis[128];     /* the axis of each frequency, < n_axes */
+} pkv_rotary;
+
+/* pkv_append_kv with the position rotation applied on the way: q and k_new are rotated (above),
+ * rotated queries written to q_out, rotated keys and the values at their slots of the pool.
+ * (The pages have no counterpart of the rotation; the write is pkv_append_kv's.)
+ *   q [n_tok][H_q][d_head], k_new, v_new [n_tok][H_kv][d_head]: device, activation type; a
+ *     token's heads are contiguous, its rows *_stride elements apart (>= the row's size), so
+ *     that parts of a fused projection's rows are taken as they lie.
+ *   q_out: as q, rows q_out_stride apart; q itself with the same stride rotates in place, any
+ *     other overlap with an input is not allowed.  q and q_out NULL: keys and values only.
+ *   positions: device int32 [n_axes][n_tok], any values; the angle is exact to about 2^-24 of a
+ *     turn over the whole range (inv_freq <= 1).
+ *   slot_mapping: device int32 [n_tok], distinct; a slot outside [0, N*B) is recorded in the
+ *     device error word (code 1) and its key and value are skipped (its query is still rotated).
+ *   layer >= 0 (one layer: positions rotate every layer's own keys).
+ * The rotation is computed in binary32 and rounded once: q_out and 16-bit keys to nearest, E4M3
+ * keys to the code nearest to the quotient rotated / k_scale.  Values are stored as pkv_append_kv
+ * stores them.  One kernel launch; no workspace.
+ * Errors: INVALID_ARG (layer, rotary_dim, n_axes, an axis >= n_axes, a stride, NULL buffers, q
+ * without q_out, buffers not aligned to their elements). */
+int pkv_append_kv_rotary(const pkv_pool* pool, int32_t layer, const pkv_rotary* rotary, const void* q,
+                         int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         const int32_t* positions, const int32_t* slot_mapping, int32_t n_tok, void* q_out,
+                         int64_t q_out_stride, void* k_pool, void* v_pool, pkv_stream_t stream);
+
 /* Bytes of device workspace pkv_decode_attention needs for n_seq sequences on
  * the current device (with prefix sharing on, also room for the shared-prefix
  * partials of a decode step of n_seq sequences). */

@@ -19,7 +19,7 @@ __all__ = [
     "PkvError", "Geometry", "Pool", "library_path", "F32", "F16", "BF16",
     "pkv_version", "pkv_pool_create", "pkv_pool_destroy", "pkv_pool_geometry", "pkv_seq_create", "pkv_seq_fork",
     "pkv_seq_free", "pkv_seq_len", "pkv_plan_append", "pkv_export_tables", "pkv_refcounts", "pkv_free_list",
-    "pkv_append_kv", "pkv_decode_workspace_size", "pkv_decode_attention", "pkv_decode_attention_noalloc",
+    "pkv_append_kv", "Rotary", "RotaryConfig", "pkv_append_kv_rotary", "pkv_decode_workspace_size", "pkv_decode_attention", "pkv_decode_attention_noalloc",
     "pkv_decode_step", "pkv_decode_step_host", "pkv_step_plan", "pkv_step_launch", "pkv_step_launch_host",
     "StepLauncher", "PackedStepLauncher",
     "pkv_prefill_attention",
@@ -51,6 +51,13 @@ class Geometry(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
                 ("d_head", ctypes.c_int32), ("block_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("num_blocks", ctypes.c_int64)]
+
+
+class RotaryConfig(ctypes.Structure):
+    """pkv_rotary (see pkv.h); ``Rotary`` fills it."""
+
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
 
 
 class PrefixStats(ctypes.Structure):
@@ -99,6 +106,8 @@ def _L():
             "pkv_refcounts": ([vp, P32], ctypes.c_int),
             "pkv_free_list": ([vp, P32, P64], ctypes.c_int),
             "pkv_append_kv": ([vp, i32, vp, vp, vp, i32, vp, vp, vp], ctypes.c_int),
+            "pkv_append_kv_rotary": ([vp, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, vp, vp],
+                                     ctypes.c_int),
             "pkv_decode_workspace_size": ([vp, i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
             "pkv_decode_attention": ([vp, i32, vp, vp, vp, vp, i32, vp, i32, ctypes.c_float, vp, vp, ctypes.c_size_t,
                                       vp], ctypes.c_int),
@@ -220,6 +229,8 @@ class Pool:
         self.handle = handle
         self.geometry = geometry
         self._meta_ints = {}  # (n, W) -> step metadata int32 count (cleared when sharing changes)
+        g = geometry
+        self._kv_elems = g.num_blocks * g.L * g.H_kv * g.block_size * g.d_head  # elements of k_pool (or v_pool)
 
     @property
     def _as_parameter_(self):
@@ -424,6 +435,112 @@ def pkv_append_kv(pool: PoolLike, layer: int, k_new, v_new, slot_mapping, k_pool
     _check(_L().pkv_append_kv(_h(pool), layer, _dev(k_new, "k_new"), _dev(v_new, "v_new"),
                               _dev(slot_mapping, "slot_mapping"), n_tok, _dev(k_pool, "k_pool"),
                               _dev(v_pool, "v_pool"), _stream(stream)), "pkv_append_kv")
+
+
+_TORCH_TYPES = {}  # pool dtype -> (activation dtype, dtypes a pool tensor may have); filled at the first use
+
+
+def _types(dtype: int):
+    if not _TORCH_TYPES:
+        import torch
+
+        f8 = (torch.uint8, torch.float8_e4m3fn)
+        _TORCH_TYPES.update({F32: (torch.float32, (torch.float32,)), F16: (torch.float16, (torch.float16,)),
+                             BF16: (torch.bfloat16, (torch.bfloat16,)), E4M3: (torch.bfloat16, f8), "i32": torch.int32})
+    return _TORCH_TYPES[dtype]
+
+
+def _current_device() -> int:
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _dev_as(t, what: str, dtypes, device: int) -> int:
+    """Device pointer of a contiguous CUDA tensor of one of dtypes on the current device."""
+    p = _dev(t, what)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} is {t.dtype}, not {' or '.join(str(x) for x in dtypes)}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    return p
+
+
+def _pools(pool: Pool, k_pool, v_pool, device: int):
+    """Pointers of the two pool tensors (their type, device and size checked)."""
+    dtypes = _types(pool.geometry.dtype)[1]
+    k, v = _dev_as(k_pool, "k_pool", dtypes, device), _dev_as(v_pool, "v_pool", dtypes, device)
+    for t, what in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t.numel() < pool._kv_elems:
+            raise ValueError(f"{what} holds {t.numel()} elements; the pool has {pool._kv_elems}")
+    return k, v
+
+
+def _rows(t, what: str, n: int, heads: int, d: int, dtype, device: int):
+    """(pointer, elements between rows) of [n][heads][d] rows whose heads lie side by side."""
+    if not hasattr(t, "is_cuda") or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} is {t.dtype}, not {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    if tuple(t.shape) != (n, heads, d):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(n, heads, d)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return t.data_ptr(), s0 if n > 1 else heads * d
+
+
+class Rotary:
+    """Rotary positions for pkv_append_kv_rotary: inv_freq, a CUDA float32 tensor with one entry per
+    rotated pair (rotary_dim / 2); interleaved: pairs are adjacent elements instead of
+    (i, i + rotary_dim / 2); axes: the position axis of each frequency (default: one axis for all).
+    Holds a reference to inv_freq."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, axes: Optional[Sequence[int]] = None,
+                 n_axes: Optional[int] = None):
+        import torch
+
+        _dev(inv_freq, "inv_freq")
+        ptr = _dev_as(inv_freq, "inv_freq", (torch.float32,), inv_freq.get_device())
+        half = inv_freq.numel()
+        if not 1 <= half <= 128:
+            raise ValueError("inv_freq must have 1 to 128 entries")
+        ax = [0] * half if axes is None else [int(x) for x in axes]
+        if len(ax) != half or min(ax) < 0 or max(ax) > 3:
+            raise ValueError("axes must name an axis in [0, 4) for every entry of inv_freq")
+        self.inv_freq = inv_freq
+        self.n_axes = max(ax) + 1 if n_axes is None else int(n_axes)
+        self.config = RotaryConfig(ptr, 2 * half, int(bool(interleaved)), self.n_axes, (ctypes.c_uint8 * 128)(*ax))
+        self._addr = ctypes.addressof(self.config)
+
+
+def pkv_append_kv_rotary(pool: Pool, layer: int, rotary: Rotary, q, k_new, v_new, positions, slot_mapping, q_out,
+                         k_pool, v_pool, stream=None) -> None:
+    """Rotate q and k_new by their positions, write rotated q to q_out (may be q) and rotated keys
+    and the values at their slots.  q, q_out [n][H_q][d], k_new, v_new [n][H_kv][d]: rows may be
+    strided (parts of a fused projection); positions int32 [n_axes][n] ([n] with one axis); q and
+    q_out None: keys and values only."""
+    g = pool.geometry
+    dev = _current_device()
+    act, i32 = _types(g.dtype)[0], (_types("i32"),)
+    n = slot_mapping.numel()
+    if positions.numel() != rotary.n_axes * n or (positions.dim() != 2 and rotary.n_axes > 1):
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, not {(rotary.n_axes, n)}")
+    if rotary.inv_freq.get_device() != dev:
+        raise ValueError(f"inv_freq is on cuda:{rotary.inv_freq.get_device()}, the current device is cuda:{dev}")
+    qp = qs = op = os_ = None
+    if q is not None or q_out is not None:
+        qp, qs = _rows(q, "q", n, g.H_q, g.d_head, act, dev)
+        op, os_ = _rows(q_out, "q_out", n, g.H_q, g.d_head, act, dev)
+    kn, ks = _rows(k_new, "k_new", n, g.H_kv, g.d_head, act, dev)
+    vn, vs = _rows(v_new, "v_new", n, g.H_kv, g.d_head, act, dev)
+    kp, vp = _pools(pool, k_pool, v_pool, dev)
+    _check(_L().pkv_append_kv_rotary(pool.handle, layer, rotary._addr, qp, qs or 0, kn, ks, vn, vs,
+                                     _dev_as(positions, "positions", i32, dev),
+                                     _dev_as(slot_mapping, "slot_mapping", i32, dev), n, op, os_ or 0, kp, vp,
+                                     _stream(stream)), "pkv_append_kv_rotary")
 
 
 def pkv_decode_workspace_size(pool: PoolLike, n_seq: int) -> int:

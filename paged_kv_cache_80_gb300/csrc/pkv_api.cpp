@@ -479,6 +479,41 @@ int pkv_append_kv(const pkv_pool* pool, int32_t layer, const void* k_new, const 
   return pkv::launch_append(P, layer, k_new, v_new, slot_mapping, n_tok, k_pool, v_pool, stream);
 }
 
+int pkv_append_kv_rotary(const pkv_pool* pool, int32_t layer, const pkv_rotary* rotary, const void* q,
+                         int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         const int32_t* positions, const int32_t* slot_mapping, int32_t n_tok, void* q_out,
+                         int64_t q_out_stride, void* k_pool, void* v_pool, pkv_stream_t stream) {
+  pkv::clear_error();
+  if (!pool || !rotary || n_tok < 0) return fail(PKV_ERR_INVALID_ARG, "bad arguments to pkv_append_kv_rotary");
+  const Pool& P = *as_pool(pool);
+  const pkv_geometry& g = P.geo;
+  if (layer < 0 || layer >= g.L) return fail(PKV_ERR_INVALID_ARG, "layer out of range");
+  if (rotary->rotary_dim < 2 || rotary->rotary_dim % 2 || rotary->rotary_dim > g.d_head)
+    return fail(PKV_ERR_INVALID_ARG, "rotary_dim must be even and in [2, d_head]");
+  if (rotary->interleaved != 0 && rotary->interleaved != 1)
+    return fail(PKV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (rotary->n_axes < 1 || rotary->n_axes > 4) return fail(PKV_ERR_INVALID_ARG, "n_axes must be in [1, 4]");
+  for (int i = 0; i < rotary->rotary_dim / 2; ++i)
+    if (rotary->axis[i] >= rotary->n_axes)
+      return fail(PKV_ERR_INVALID_ARG, "the axis of frequency " + std::to_string(i) + " is not below n_axes");
+  if (n_tok == 0) return PKV_OK;
+  if (!k_new || !v_new || !positions || !slot_mapping || !k_pool || !v_pool || !rotary->inv_freq)
+    return fail(PKV_ERR_INVALID_ARG, "NULL buffer");
+  if (!q != !q_out) return fail(PKV_ERR_INVALID_ARG, "q and q_out are given together or not at all");
+  const int64_t q_row = static_cast<int64_t>(g.H_q) * g.d_head, kv_row = static_cast<int64_t>(g.H_kv) * g.d_head;
+  if (k_stride < kv_row || v_stride < kv_row || (q && (q_stride < q_row || q_out_stride < q_row)))
+    return fail(PKV_ERR_INVALID_ARG, "a row stride is smaller than the row");
+  if (q && q_out == q && q_out_stride != q_stride)
+    return fail(PKV_ERR_INVALID_ARG, "rotating q in place needs q_out_stride == q_stride");
+  const uintptr_t act = static_cast<uintptr_t>(pkv::act_size(g.dtype)), elem = static_cast<uintptr_t>(pkv::elem_size(g.dtype));
+  const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if ((at(q) | at(q_out) | at(k_new) | at(v_new)) & (act - 1) || (at(k_pool) | at(v_pool)) & (elem - 1) ||
+      (at(positions) | at(slot_mapping) | at(rotary->inv_freq)) & 3)
+    return fail(PKV_ERR_INVALID_ARG, "a buffer is not aligned to its elements");
+  return pkv::launch_append_rotary(P, layer, *rotary, q, q_stride, k_new, k_stride, v_new, v_stride, positions,
+                                   slot_mapping, n_tok, q_out, q_out_stride, k_pool, v_pool, stream);
+}
+
 int pkv_decode_workspace_size(const pkv_pool* pool, int32_t n_seq, size_t* bytes) {
   pkv::clear_error();
   if (!pool || !bytes || n_seq < 0) return fail(PKV_ERR_INVALID_ARG, "bad arguments");

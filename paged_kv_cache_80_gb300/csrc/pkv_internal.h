@@ -130,6 +130,12 @@ struct CopyItem {
 int launch_append(const Pool& P, int32_t layer, const void* k_new, const void* v_new, const int32_t* slots,
                   int32_t n_tok, void* k_pool, void* v_pool, void* stream, bool lets_dependents = false);
 
+// The append with rotary positions (pkv_append_kv_rotary); q and q_out may be null.
+int launch_append_rotary(const Pool& P, int32_t layer, const pkv_rotary& rot, const void* q, int64_t q_stride,
+                         const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         const int32_t* positions, const int32_t* slots, int32_t n_tok, void* q_out,
+                         int64_t q_out_stride, void* k_pool, void* v_pool, void* stream);
+
 // Copy `n` contiguous images of `bytes` bytes each, image i from src_base +
 // items[i].src_off to dst_base + items[i].dst_off (device-accessible pointers).  max_ctas > 0:
 // from at most that many CTAs (a copy that runs beside compute), else one CTA per 128 KiB.
