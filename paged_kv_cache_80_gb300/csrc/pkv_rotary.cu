@@ -125,6 +125,163 @@ __global__ void __launch_bounds__(256) rotary_append_any_kernel(const __grid_con
   }
 }
 
+// Rows made of 16-byte vectors (d_head and rotary_dim multiples of 2 E, E elements a vector; every row and
+// pool on a 16-byte boundary).  A thread handles chunk c of a row, two vectors that hold both elements of E
+// pairs: elements E c .. and rotary_dim / 2 + E c .. of a rotated head in halves, 2 E c .. (adjacent pairs), or
+// 2 E neighbours past rotary_dim; c stays the same for all of a thread's rows.  A CTA takes tiles of
+// `tokens` tokens (or, when there are few, one split of one token's rows): its first rows' vectors are on
+// their way while each thread makes the cosines and sines of one frequency, which all H_q + H_kv heads of a
+// token share through shared memory, as float4 entries [token][E / 2][chunk] that neighbouring threads read
+// without bank conflicts.  The work is the bytes moved: everything else has to hide behind them.
+template <typename TA>
+struct RowVec {
+  static constexpr int E = 16 / sizeof(TA);
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&f)[E]) {
+    const TA* p = reinterpret_cast<const TA*>(&w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = to_f(p[e]);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[E]) {
+    uint4 w;
+    if constexpr (E == 4) {
+      w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+      w = make_uint4(pack2<TA>(f[0], f[1]), pack2<TA>(f[2], f[3]), pack2<TA>(f[4], f[5]), pack2<TA>(f[6], f[7]));
+    }
+    return w;
+  }
+};
+
+// eight values to E4M3 codes of x / scale
+__device__ __forceinline__ uint2 codes_of(const float (&f)[8], float scale) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e >> 2] |= static_cast<uint32_t>(e4m3_of(f[e], scale)) << (8 * (e & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+constexpr int kRotThreads = 256;
+constexpr int kRotUnroll = 2;  // rows a thread has in flight
+
+template <typename TA, bool F8, bool INTER>
+__global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const __grid_constant__ RotaryArgs a, int tokens,
+                                                                     int splits) {
+  using RV = RowVec<TA>;
+  constexpr int E = RV::E, U = kRotUnroll;
+  extern __shared__ float4 cs4[];  // [tokens][E / 2][nch]: (cos, sin) of two frequencies
+  const int half = a.rot / 2, nch = half / E, nct = a.d / (2 * E), all_rows = a.H_q + 2 * a.H_kv;
+  const int first_row = a.q ? 0 : a.H_q;
+  const int per = (all_rows - first_row + splits - 1) / splits;
+  const int tid = threadIdx.x;
+  const int c = tid % nct, r0 = tid / nct, rpp = kRotThreads / nct;
+  const int o0 = c >= nch ? a.rot + 2 * E * (c - nch) : (INTER ? 2 * E * c : E * c);
+  const int o1 = c >= nch || INTER ? o0 + E : half + E * c;
+  const int fi = tid % half, ft = tid / half, tpp = kRotThreads / half;  // this thread's frequency and first token
+  unsigned long long u = 0;
+  const int32_t* pos = a.positions + static_cast<int64_t>(a.axis[fi]) * a.n_tok;
+  float2* cs_out = reinterpret_cast<float2*>(cs4) + (((fi % E) / 2) * nch + fi / E) * 2 + (fi & 1);
+  const int tiles = (a.n_tok + tokens - 1) / tokens;
+  bool first = true;
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(tiles) * splits; w += gridDim.x) {
+    const int tile = static_cast<int>(w / splits), sp = static_cast<int>(w - static_cast<int64_t>(tile) * splits);
+    const int64_t t0 = static_cast<int64_t>(tile) * tokens;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), a.n_tok - t0));
+    const int rb = first_row + sp * per, nr = min(all_rows, rb + per) - rb;  // this split's rows
+    int t = 0, row = r0;  // the next row to load: token t of the tile, row rb + row
+    auto settle = [&] {
+      while (row >= nr && t < nt) {
+        row -= nr;
+        ++t;
+      }
+    };
+    if (r0 >= rpp || nr <= 0) t = nt;
+    settle();
+    uint4 x0[U], x1[U];
+    int xt[U], xr[U];
+    auto load = [&](int k) {
+      xt[k] = t;
+      xr[k] = rb + row;
+      if (t >= nt) return;
+      const int64_t tok = t0 + t;
+      const int r = rb + row;
+      const TA* src = r < a.H_q ? static_cast<const TA*>(a.q) + tok * a.q_stride + static_cast<int64_t>(r) * a.d
+                      : r < a.H_q + a.H_kv
+                          ? static_cast<const TA*>(a.k) + tok * a.k_stride + static_cast<int64_t>(r - a.H_q) * a.d
+                          : static_cast<const TA*>(a.v) + tok * a.v_stride + static_cast<int64_t>(r - a.H_q - a.H_kv) * a.d;
+      x0[k] = *reinterpret_cast<const uint4*>(src + o0);
+      x1[k] = *reinterpret_cast<const uint4*>(src + o1);
+      row += rpp;
+      settle();
+    };
+#pragma unroll
+    for (int k = 0; k < U; ++k) load(k);
+    if (first) u = turns_of(a.inv_freq[fi]);
+    else __syncthreads();  // every thread is done with the last tile's angles
+    first = false;
+    if (ft < tpp)
+      for (int k = ft; k < nt; k += tpp) cs_out[static_cast<int64_t>(k) * half] = cos_sin(u, pos[t0 + k]);
+    __syncthreads();
+    while (xt[0] < nt) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (xt[k] >= nt) break;
+        const int64_t tok = t0 + xt[k];
+        const int r = xr[k];
+        const bool is_v = r >= a.H_q + a.H_kv;
+        float f0[E], f1[E];
+        RV::unpack(x0[k], f0);
+        RV::unpack(x1[k], f1);
+        if (c < nch && !is_v) {
+          const float4* cs = cs4 + static_cast<int64_t>(xt[k]) * (E / 2) * nch + c;
+#pragma unroll
+          for (int j = 0; j < E / 2; ++j) {
+            const float4 v = cs[j * nch];
+            if constexpr (INTER) {  // pairs (2i, 2i + 1): frequencies E c + 2j, + 1 lie in elements 4j .. 4j + 3 of the chunk
+              float* f = 4 * j < E ? f0 + 4 * j : f1 + (4 * j - E);
+              const float a0 = f[0], a1 = f[1], b0 = f[2], b1 = f[3];
+              f[0] = a0 * v.x - a1 * v.y;
+              f[1] = a1 * v.x + a0 * v.y;
+              f[2] = b0 * v.z - b1 * v.w;
+              f[3] = b1 * v.z + b0 * v.w;
+            } else {
+              const float a0 = f0[2 * j], a1 = f1[2 * j], b0 = f0[2 * j + 1], b1 = f1[2 * j + 1];
+              f0[2 * j] = a0 * v.x - a1 * v.y;
+              f1[2 * j] = a1 * v.x + a0 * v.y;
+              f0[2 * j + 1] = b0 * v.z - b1 * v.w;
+              f1[2 * j + 1] = b1 * v.z + b0 * v.w;
+            }
+          }
+        }
+        if (r < a.H_q) {
+          TA* dst = static_cast<TA*>(a.q_out) + tok * a.q_out_stride + static_cast<int64_t>(r) * a.d;
+          *reinterpret_cast<uint4*>(dst + o0) = RV::pack(f0);
+          *reinterpret_cast<uint4*>(dst + o1) = RV::pack(f1);
+        } else {
+          const int32_t slot = a.slots[tok];
+          const int h = is_v ? r - a.H_q - a.H_kv : r - a.H_q;
+          if (slot < 0 || slot >= a.n_slots) {
+            if (c == 0 && h == 0 && !is_v) record_error(a.err, DERR_APPEND_SLOT, slot);
+          } else {
+            const int64_t blk = slot / a.B, off = slot - blk * a.B;
+            const int64_t at = (((blk * a.L + a.layer) * a.H_kv + h) * a.B + off) * a.d;
+            void* pool = is_v ? a.v_pool : a.k_pool;
+            if constexpr (F8) {
+              const float scale = is_v ? a.v_scale : a.k_scale;
+              *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at + o0) = codes_of(f0, scale);
+              *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at + o1) = codes_of(f1, scale);
+            } else {
+              *reinterpret_cast<uint4*>(static_cast<TA*>(pool) + at + o0) = RV::pack(f0);
+              *reinterpret_cast<uint4*>(static_cast<TA*>(pool) + at + o1) = RV::pack(f1);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) load(k);
+    }
+  }
+}
+
 int sm_count() {
   static int cache[64] = {0};
   int dev = 0;
@@ -137,12 +294,38 @@ int sm_count() {
   return cache[dev];
 }
 
-template <typename TA, bool F8>
-void launch_t(const RotaryArgs& a, bool interleaved, cudaStream_t st) {
-  const int64_t items = static_cast<int64_t>(a.n_tok) * (a.H_q + 2 * a.H_kv) * (a.d / 2);
-  const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(sm_count()) * 8));
-  if (interleaved) rotary_append_any_kernel<TA, F8, true><<<grid, 256, 0, st>>>(a);
-  else rotary_append_any_kernel<TA, F8, false><<<grid, 256, 0, st>>>(a);
+// Whether every row is made of whole 16-byte vectors on 16-byte boundaries (the vector kernel's rows).
+bool vector_rows(const RotaryArgs& a, int act, int elem) {
+  const int E = 16 / act;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out) |
+                      reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                      static_cast<uintptr_t>((a.q_stride | a.k_stride | a.v_stride | a.q_out_stride) * act);
+  const uintptr_t pools = reinterpret_cast<uintptr_t>(a.k_pool) | reinterpret_cast<uintptr_t>(a.v_pool);
+  return a.d % (2 * E) == 0 && a.rot % (2 * E) == 0 && p % 16 == 0 && pools % (E * elem) == 0;
+}
+
+template <typename TA, bool F8, bool INTER>
+void launch_t(const RotaryArgs& a, cudaStream_t st) {
+  constexpr int E = RowVec<TA>::E;
+  const int64_t sms = sm_count();
+  if (!vector_rows(a, sizeof(TA), F8 ? 1 : sizeof(TA))) {
+    const int64_t items = static_cast<int64_t>(a.n_tok) * (a.H_q + 2 * a.H_kv) * (a.d / 2);
+    const int grid = static_cast<int>(std::min<int64_t>((items + 255) / 256, sms * 8));
+    rotary_append_any_kernel<TA, F8, INTER><<<grid, 256, 0, st>>>(a);
+    return;
+  }
+  // Few tokens: each thread one row, a token's rows over several CTAs.  Otherwise tiles of up to
+  // kTokens tokens for a grid that stays resident (4 CTAs an SM).
+  constexpr int kTokens = 4;
+  const int rows = (a.q ? a.H_q : 0) + 2 * a.H_kv, rpp = kRotThreads / (a.d / (2 * E));
+  const int64_t passes = (rows + rpp - 1) / rpp;
+  int tokens = 1, splits = 1;
+  if (a.n_tok * passes <= sms * 8) splits = static_cast<int>(passes);
+  else tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTokens, a.n_tok / (sms * 4))));
+  const int64_t work = static_cast<int64_t>((a.n_tok + tokens - 1) / tokens) * splits;
+  const int grid = static_cast<int>(std::min<int64_t>(work, splits > 1 ? sms * 8 : sms * 4));
+  const size_t smem = static_cast<size_t>(tokens) * a.rot / 2 * sizeof(float2);
+  rotary_append_kernel<TA, F8, INTER><<<grid, kRotThreads, smem, st>>>(a, tokens, splits);
 }
 
 }  // namespace
@@ -184,10 +367,10 @@ int launch_append_rotary(const Pool& P, int32_t layer, const pkv_rotary& rot, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool inter = rot.interleaved != 0;
   switch (g.dtype) {
-    case PKV_F32: launch_t<float, false>(a, inter, st); break;
-    case PKV_F16: launch_t<__half, false>(a, inter, st); break;
-    case PKV_BF16: launch_t<__nv_bfloat16, false>(a, inter, st); break;
-    default: launch_t<__nv_bfloat16, true>(a, inter, st); break;
+    case PKV_F32: inter ? launch_t<float, false, true>(a, st) : launch_t<float, false, false>(a, st); break;
+    case PKV_F16: inter ? launch_t<__half, false, true>(a, st) : launch_t<__half, false, false>(a, st); break;
+    case PKV_BF16: inter ? launch_t<__nv_bfloat16, false, true>(a, st) : launch_t<__nv_bfloat16, false, false>(a, st); break;
+    default: inter ? launch_t<__nv_bfloat16, true, true>(a, st) : launch_t<__nv_bfloat16, true, false>(a, st); break;
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("rotary append launch: ") + cudaGetErrorString(e));
