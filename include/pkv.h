@@ -433,6 +433,30 @@ int pkv_prefill_attention(const pkv_pool* pool, int32_t layer, const void* q, co
                           int32_t max_q, const void* k_pool, const void* v_pool, const int32_t* block_tables, int32_t W,
                           const int32_t* seq_lens, int32_t n_seq, float scale, void* out, pkv_stream_t stream);
 
+/* Attention with a sliding window and sinks: the first tokens that stay visible.  (The pages have
+ * no counterpart of the mask; everything else is pkv_decode_attention's and
+ * pkv_prefill_attention's.)  The query at position p sees the keys t <= p with
+ *   t > p - window   (the last `window` keys, its own among them)   or   t < n_sink,
+ * and its softmax runs over those.  window >= 1, n_sink >= 0; both may exceed every length.
+ * Keys that no query of the call sees have no effect whatever their bytes, and the blocks that
+ * hold none of the others are neither read nor looked up: their table entries may hold anything.
+ * pkv_decode_attention_window: one query per sequence, at position len_s - 1.  Arguments, types,
+ *   workspace, kernels and limits as for pkv_decode_attention; batches lay out only the 16-token
+ *   tiles that hold a visible key, so every warp reads the same number of visible bytes.
+ * pkv_prefill_attention_window: the queries of a chunk, each with its own window.  Arguments, types,
+ *   kernels and limits as for pkv_prefill_attention; rows of q and out past q_offsets[n_seq] are
+ *   neither read nor written.  A key that one query of the chunk sees and another does not must
+ *   be finite, as in pkv_prefill_attention: 0 times its value reaches rows of the same tile.
+ * scale must be finite and > 0.  The calls may be captured into a graph and replayed. */
+int pkv_decode_attention_window(const pkv_pool* pool, int32_t layer, const void* q, const void* k_pool,
+                                const void* v_pool, const int32_t* block_tables, int32_t W, const int32_t* seq_lens,
+                                int32_t n_seq, int32_t window, int32_t n_sink, float scale, void* out,
+                                void* workspace, size_t ws_bytes, pkv_stream_t stream);
+int pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q, const int32_t* q_offsets,
+                                 int32_t n_tok, int32_t max_q, const void* k_pool, const void* v_pool,
+                                 const int32_t* block_tables, int32_t W, const int32_t* seq_lens, int32_t n_seq,
+                                 int32_t window, int32_t n_sink, float scale, void* out, pkv_stream_t stream);
+
 /* Copy-on-write data step ([KVM] "copies the B tokens from the shared block into
  * p_new"): for each (src, dst) in pairs (HOST int32 [n][2]), copy every slot of
  * every layer of block src into block dst, for K and V.  Pairs are passed to the
@@ -624,7 +648,7 @@ int pkv_device_code_version(int32_t* binary_version, int32_t* ptx_version);
  * Returns DEVICE_CHECK if a kernel recorded a bad index since the last check;
  * *code and *detail (the offending value) describe it: 1 a slot out of range (append),
  * 2 a sequence length < 0 or > W * B, 3 a block id out of range in a table, 4 a bounded
- * wait that gave up (detail: where), 6 a prefill chunk longer than max_q, 7 a
+ * wait that gave up (detail: where), 6 a prefill chunk longer than max_q or outside q's rows, 7 a
  * shared-prefix plan entry out of range (detail: the sequence or work item).
  * Either output pointer may be NULL. */
 int pkv_check_device_error(pkv_stream_t stream, int32_t* code, int64_t* detail);

@@ -20,7 +20,7 @@ __all__ = [
     "pkv_version", "pkv_pool_create", "pkv_pool_destroy", "pkv_pool_geometry", "pkv_seq_create", "pkv_seq_fork",
     "pkv_seq_free", "pkv_seq_len", "pkv_plan_append", "pkv_export_tables", "pkv_refcounts", "pkv_free_list",
     "pkv_append_kv", "Rotary", "RotaryConfig", "pkv_append_kv_rotary", "pkv_decode_workspace_size", "pkv_decode_attention", "pkv_decode_attention_noalloc",
-    "pkv_decode_step", "pkv_decode_step_host", "pkv_step_plan", "pkv_step_launch", "pkv_step_launch_host",
+    "pkv_decode_attention_window", "pkv_prefill_attention_window", "pkv_decode_step", "pkv_decode_step_host", "pkv_step_plan", "pkv_step_launch", "pkv_step_launch_host",
     "StepLauncher", "PackedStepLauncher",
     "pkv_prefill_attention",
     "pkv_copy_blocks", "pkv_swap_out",
@@ -113,6 +113,10 @@ def _L():
                                       vp], ctypes.c_int),
             "pkv_decode_attention_noalloc": ([vp, i32, vp, vp, vp, vp, i32, vp, i32, ctypes.c_float, vp, vp],
                                              ctypes.c_int),
+            "pkv_decode_attention_window": ([vp, i32, vp, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, vp,
+                                             ctypes.c_size_t, vp], ctypes.c_int),
+            "pkv_prefill_attention_window": ([vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp, i32, i32, i32,
+                                              ctypes.c_float, vp, vp], ctypes.c_int),
             "pkv_copy_blocks": ([vp, P32, i32, vp, vp, vp], ctypes.c_int),
             "pkv_prefill_attention": ([vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp, i32, ctypes.c_float, vp, vp],
                                       ctypes.c_int),
@@ -788,6 +792,48 @@ def pkv_prefill_attention(pool: PoolLike, layer: int, q, q_offsets, max_q: int, 
                                       int(max_q), _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"),
                                       _dev(block_tables, "block_tables"), W, _dev(seq_lens, "seq_lens"), n_seq,
                                       float(scale), _dev(out, "out"), _stream(stream)), "pkv_prefill_attention")
+
+
+def _attention_args(pool: Pool, q, k_pool, v_pool, block_tables, seq_lens, out, rows: int, device: int):
+    """Pointers of a windowed attention call's tensors, their types, shapes and device checked:
+    (q, k_pool, v_pool, block_tables, W, seq_lens, n_seq, out)."""
+    g = pool.geometry
+    act, i32 = (_types(g.dtype)[0],), (_types("i32"),)
+    qp, op = _dev_as(q, "q", act, device), _dev_as(out, "out", act, device)
+    for t, what in ((q, "q"), (out, "out")):
+        if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != g.H_q or t.shape[2] != g.d_head:
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, g.H_q, g.d_head)}")
+    kp, vp = _pools(pool, k_pool, v_pool, device)
+    tp, lp = _dev_as(block_tables, "block_tables", i32, device), _dev_as(seq_lens, "seq_lens", i32, device)
+    n = seq_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError(f"block_tables has shape {tuple(block_tables.shape)}, not ({n}, W)")
+    return qp, kp, vp, tp, block_tables.shape[1], lp, n, op
+
+
+def pkv_decode_attention_window(pool: Pool, layer: int, q, k_pool, v_pool, block_tables, seq_lens, window: int,
+                                n_sink: int, scale: float, out, workspace, stream=None) -> None:
+    """pkv_decode_attention over the last `window` keys of each sequence and its first `n_sink`."""
+    dev = _current_device()
+    qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out,
+                                                   seq_lens.numel(), dev)
+    _check(_L().pkv_decode_attention_window(pool.handle, layer, qp, kp, vp, tp, W, lp, n, window, n_sink, scale, op,
+                                            _dev(workspace, "workspace"), _nbytes(workspace), _stream(stream)),
+           "pkv_decode_attention_window")
+
+
+def pkv_prefill_attention_window(pool: Pool, layer: int, q, q_offsets, max_q: int, k_pool, v_pool, block_tables,
+                                 seq_lens, window: int, n_sink: int, scale: float, out, stream=None) -> None:
+    """pkv_prefill_attention in which the query at position p sees its last `window` keys and the
+    sequence's first `n_sink`; rows of q and out past q_offsets[n_seq] are left alone."""
+    dev = _current_device()
+    qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, q.shape[0], dev)
+    offs = _dev_as(q_offsets, "q_offsets", (_types("i32"),), dev)
+    if q_offsets.numel() != n + 1:
+        raise ValueError(f"q_offsets has {q_offsets.numel()} entries, not {n + 1}")
+    _check(_L().pkv_prefill_attention_window(pool.handle, layer, qp, offs, q.shape[0], max_q, kp, vp, tp, W, lp, n,
+                                             window, n_sink, scale, op, _stream(stream)),
+           "pkv_prefill_attention_window")
 
 
 def pkv_copy_blocks(pool: PoolLike, pairs, k_pool, v_pool, stream=None) -> None:

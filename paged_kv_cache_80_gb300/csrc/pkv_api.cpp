@@ -551,6 +551,50 @@ int pkv_prefill_attention(const pkv_pool* pool, int32_t layer, const void* q, co
                              W, seq_lens, n_seq, scale, out, stream);
 }
 
+// The window arguments of the windowed attention calls.
+static int window_check(int32_t window, int32_t n_sink, float scale) {
+  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window must be at least 1");
+  if (n_sink < 0) return fail(PKV_ERR_INVALID_ARG, "n_sink must not be negative");
+  if (!(std::isfinite(scale) && scale > 0.f)) return fail(PKV_ERR_INVALID_ARG, "scale must be finite and > 0");
+  return PKV_OK;
+}
+
+int pkv_decode_attention_window(const pkv_pool* pool, int32_t layer, const void* q, const void* k_pool,
+                                const void* v_pool, const int32_t* block_tables, int32_t W, const int32_t* seq_lens,
+                                int32_t n_seq, int32_t window, int32_t n_sink, float scale, void* out,
+                                void* workspace, size_t ws_bytes, pkv_stream_t stream) {
+  pkv::clear_error();
+  if (!pool || n_seq < 0 || W < 0) return fail(PKV_ERR_INVALID_ARG, "bad arguments to pkv_decode_attention_window");
+  const Pool& P = *as_pool(pool);
+  if (layer < 0 || layer >= P.geo.L) return fail(PKV_ERR_INVALID_ARG, "layer out of range");
+  if (int rc = window_check(window, n_sink, scale)) return rc;
+  if (n_seq == 0) return PKV_OK;
+  if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out || !workspace)
+    return fail(PKV_ERR_INVALID_ARG, "NULL buffer");
+  return pkv::launch_decode(const_cast<Pool&>(P), layer, q, k_pool, v_pool, block_tables, W, seq_lens, n_seq, scale,
+                            out, workspace, ws_bytes, stream, nullptr, nullptr, false, pkv::Window{window, n_sink});
+}
+
+int pkv_prefill_attention_window(const pkv_pool* pool, int32_t layer, const void* q, const int32_t* q_offsets,
+                                 int32_t n_tok, int32_t max_q, const void* k_pool, const void* v_pool,
+                                 const int32_t* block_tables, int32_t W, const int32_t* seq_lens, int32_t n_seq,
+                                 int32_t window, int32_t n_sink, float scale, void* out, pkv_stream_t stream) {
+  pkv::clear_error();
+  if (!pool || n_seq < 0 || W < 0 || n_tok < 0 || max_q < 0)
+    return fail(PKV_ERR_INVALID_ARG, "bad arguments to pkv_prefill_attention_window");
+  const Pool& P = *as_pool(pool);
+  if (layer < 0 || layer >= P.geo.L) return fail(PKV_ERR_INVALID_ARG, "layer out of range");
+  if (int rc = window_check(window, n_sink, scale)) return rc;
+  if (n_seq == 0 || n_tok == 0) return PKV_OK;
+  if (max_q == 0) return fail(PKV_ERR_INVALID_ARG, "max_q must be at least the longest chunk");
+  if (n_seq > 65535) return fail(PKV_ERR_INVALID_ARG, "at most 65535 sequences per call");
+  if (!q || !q_offsets || !k_pool || !v_pool || !block_tables || !seq_lens || !out)
+    return fail(PKV_ERR_INVALID_ARG, "NULL buffer");
+  if (P.geo.H_q / P.geo.H_kv > 128) return fail(PKV_ERR_UNSUPPORTED, "more than 128 query heads per KV head");
+  return pkv::launch_prefill(const_cast<Pool&>(P), layer, q, q_offsets, n_tok, max_q, k_pool, v_pool, block_tables,
+                             W, seq_lens, n_seq, scale, out, stream, pkv::Window{window, n_sink});
+}
+
 int pkv_copy_blocks(const pkv_pool* pool, const int32_t* pairs, int32_t n, void* k_pool, void* v_pool,
                     pkv_stream_t stream) {
   pkv::clear_error();

@@ -34,7 +34,7 @@ struct DecodeArgs {
   const int32_t* tables;
   const int32_t* seq_lens;
   int32_t* tile_prefix;  // [n_seq + 1]: tiles of sequences before s (per KV head)
-  int32_t* lens_c;       // [n_seq]: lengths clamped to [0, W*B]
+  int32_t* lens_c;       // [n_seq]: tiles of each sequence
   int32_t* hdr;          // [0] = total tiles over all pairs
   // [total_warps]: arrivals at the split pair whose first tile lies in warp w's range, as
   // (epoch << 16) | count; a word carrying another launch's epoch counts as zero, so the
@@ -45,6 +45,7 @@ struct DecodeArgs {
   int* err;
   int64_t num_blocks;
   int32_t n_seq, W, H_q, H_kv, G, L, layer, B;
+  int32_t n_tok;     // chunked prefill: rows of q and out
   int32_t D, elem;   // head dimension, bytes per activation element (q, out)
   float scale_log2;  // scale * log2(e) (* k_scale for an FP8 pool)
   float v_mul;       // 1, or v_scale for an FP8 pool
@@ -66,7 +67,20 @@ struct DecodeArgs {
   int64_t prior_slots;  // slots prior_ml / prior_o hold
   float* sfx_ml;
   float* sfx_o;
+  // Sliding window (0: none): a query at position p sees the keys t <= p with t > p - window or
+  // t < n_sink.
+  int32_t window, n_sink;
 };
+
+// The keys that the query at position p sees: t < ns and lo <= t <= p (ns <= lo; without a window
+// ns = lo = 0).  window and n_sink are >= 0, so nothing here passes 32 bits.
+struct Visible {
+  int32_t ns, lo;
+};
+__host__ __device__ __forceinline__ Visible visible_at(int32_t window, int32_t n_sink, int32_t p) {
+  const int32_t lo = window > 0 && p >= window ? p - window + 1 : 0;
+  return Visible{n_sink < lo ? n_sink : lo, lo};
+}
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -118,13 +132,14 @@ constexpr int SIMT_WARPS = 8;
 // into the running (m, l, O) of each head with one rescale per chunk.  The warps
 // are merged in shared memory at the end.
 // Attention of the G query rows at q (contiguous, d apart) over the first len tokens
-// of sequence s, KV head g; writes G rows at out.  Run by the whole CTA.  TS is the
+// of sequence s (of which the query at len - 1 sees `vis`, walked without the gap), KV head g;
+// writes G rows at out.  Run by the whole CTA.  TS is the
 // stored K/V element, TA the q / out element; HP >= G is the head capacity (8, or 16
 // for wider groups).
 template <typename TS, typename TA, int NPL, int HP = GPAD>
 __device__ __forceinline__ void simt_attend(const DecodeArgs& a, const TS* __restrict__ kp,
-                                            const TS* __restrict__ vp, int d, int s, int g, int len, const TA* q,
-                                            TA* out) {
+                                            const TS* __restrict__ vp, int d, int s, int g, int len, Visible vis,
+                                            const TA* q, TA* out) {
   constexpr int TOK = NPL >= 8 ? 2 : (NPL >= 4 ? 4 : 8);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.G;
@@ -140,13 +155,14 @@ __device__ __forceinline__ void simt_attend(const DecodeArgs& a, const TS* __res
       o[h][j] = 0.f;
     }
   }
-  for (int t0 = warp * TOK; t0 < len; t0 += SIMT_WARPS * TOK) {
+  const int gap = vis.lo - vis.ns, n_vis = len - gap;
+  for (int t0 = warp * TOK; t0 < n_vis; t0 += SIMT_WARPS * TOK) {
     float k[TOK][NPL], v[TOK][NPL];
     bool ok[TOK];
 #pragma unroll
     for (int u = 0; u < TOK; ++u) {
-      const int t = t0 + u;
-      ok[u] = t < len;
+      const int t = t0 + u < vis.ns ? t0 + u : t0 + u + gap;
+      ok[u] = t0 + u < n_vis;
       int64_t base = 0;
       if (ok[u]) {
         int blk = a.tables[static_cast<int64_t>(s) * a.W + t / a.B];
@@ -242,7 +258,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 int get_tensor_maps(Pool& P, const void* k, const void* v, CUtensorMap* tk, CUtensorMap* tv);
 // Fields of DecodeArgs shared by every attention launch.
 int fill_args(const Pool& P, int32_t layer, const void* q, void* out, const int32_t* tables, int32_t W,
-              const int32_t* seq_lens, int32_t n_seq, float scale, DecodeArgs* a);
+              const int32_t* seq_lens, int32_t n_seq, float scale, const Window& win, DecodeArgs* a);
 // The prefix kernel of a decode step with shared prefixes (pkv_prefill.cu): one CTA per (pair
 // of 128-row tiles of the item's rows, KV head, work item); a carries share_items and prior_*.
 // Launched as the programmatic dependent of the decode kernel just before it (it reads nothing

@@ -108,6 +108,32 @@ __device__ __forceinline__ int32_t clamped_len(const DecodeArgs& a, int s, bool 
   return seq_span(a, s, record).len;
 }
 
+// With a window: the tiles of sequence s that hold a visible key -- sink tiles 0 .. sink_tiles - 1,
+// then from tile `first` on -- and which keys those are.  Every one of them has a visible key.
+struct WinTiles {
+  int32_t len, ns, lo, sink_tiles, first, n;
+  __device__ __forceinline__ int32_t token0(int32_t j) const {  // first token of the j-th of them
+    return (j < sink_tiles ? j : first + j - sink_tiles) * TILE;
+  }
+};
+__device__ __forceinline__ WinTiles win_tiles(const DecodeArgs& a, int s, bool record) {
+  WinTiles w;
+  w.len = clamped_len(a, s, record);
+  const Visible v = visible_at(a.window, a.n_sink, w.len - 1);
+  w.ns = v.ns;
+  w.lo = v.lo;
+  w.sink_tiles = (v.ns + TILE - 1) / TILE;
+  w.first = max(w.sink_tiles, v.lo / TILE);
+  w.n = w.sink_tiles + (w.len + TILE - 1) / TILE - w.first;
+  return w;
+}
+// Tiles of sequence s that the launch attends to.
+template <bool WIN>
+__device__ __forceinline__ int32_t seq_tiles(const DecodeArgs& a, int s, bool record) {
+  if constexpr (WIN) return win_tiles(a, s, record).n;
+  return (clamped_len(a, s, record) + TILE - 1) / TILE;
+}
+
 // One CTA: clamp lengths, tiles per sequence, exclusive prefix, total tile count.
 __global__ void __launch_bounds__(1024) plan_kernel(const DecodeArgs a) {
   // let the attention kernel launch now; it waits for this grid before reading its outputs
@@ -118,9 +144,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeArgs a) {
   const int s0 = min(a.n_seq, tid * per), s1 = min(a.n_seq, s0 + per);
   int32_t local = 0;
   for (int s = s0; s < s1; ++s) {
-    const int32_t len = seq_span(a, s, true).len;
-    a.lens_c[s] = len;
-    local += (len + TILE - 1) / TILE;
+    const int32_t nt = a.window > 0 ? seq_tiles<true>(a, s, true) : seq_tiles<false>(a, s, true);
+    a.lens_c[s] = nt;
+    local += nt;
   }
   // block-wide exclusive scan of `local`
   const int lane = tid & 31, warp = tid >> 5;
@@ -143,7 +169,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const DecodeArgs a) {
   int32_t run = (warp > 0 ? warp_sums[warp - 1] : 0) + incl - local;
   for (int s = s0; s < s1; ++s) {
     a.tile_prefix[s] = run;
-    run += (a.lens_c[s] + TILE - 1) / TILE;
+    run += a.lens_c[s];
   }
   if (tid == blockDim.x - 1) {
     a.tile_prefix[a.n_seq] = run;
@@ -197,7 +223,7 @@ constexpr int kSelfPlanMaxSeqs = 4096;
 // thread whose chunk of sequences holds a warp's start finds it.  CTA 0 records bad
 // lengths; CTA (s mod grid) zeroes the output of an empty sequence s.  Ends with a CTA
 // barrier, so it is called by every thread before any warp leaves.
-template <int NW>
+template <int NW, bool WIN>
 __device__ void self_plan(const DecodeArgs& a, int4* s_start, int32_t* s_q, int32_t* s_total) {
   __shared__ int32_t wsum[NW];
   constexpr int NT = NW * 32;
@@ -207,9 +233,9 @@ __device__ void self_plan(const DecodeArgs& a, int4* s_start, int32_t* s_q, int3
   const int row16 = a.H_q * a.D * a.elem / 16;
   int32_t local = 0;
   for (int s = s0; s < s1; ++s) {
-    const int32_t len = clamped_len(a, s, blockIdx.x == 0);
-    local += (len + TILE - 1) / TILE;
-    if (len == 0 && s % gridDim.x == blockIdx.x)  // an empty sequence attends to nothing: zero output
+    const int32_t nt = seq_tiles<WIN>(a, s, blockIdx.x == 0);
+    local += nt;
+    if (nt == 0 && s % gridDim.x == blockIdx.x)  // an empty sequence attends to nothing: zero output
       for (int k = 0; k < row16; ++k)
         reinterpret_cast<int4*>(static_cast<char*>(a.out) + static_cast<int64_t>(s) * row16 * 16)[k] =
             make_int4(0, 0, 0, 0);
@@ -239,7 +265,7 @@ __device__ void self_plan(const DecodeArgs& a, int4* s_start, int32_t* s_q, int3
     } else if (local > 0 && a.H_kv * excl <= start && start < a.H_kv * (excl + local)) {
       int32_t q = excl;
       for (int s = s0; s < s1; ++s) {
-        const int nt = (clamped_len(a, s, false) + TILE - 1) / TILE;
+        const int nt = seq_tiles<WIN>(a, s, false);
         if (a.H_kv * (q + nt) > start) {
           const int within = start - a.H_kv * q;
           s_start[w] = make_int4(s, within / nt, within - (within / nt) * nt, nt);
@@ -512,9 +538,13 @@ __global__ void __launch_bounds__(256) share_combine_kernel(const DecodeArgs a) 
 //   x = TMA row coordinate of the slab, y = pair id (s * H_kv + g),
 //   z = valid tokens | first-of-pair << 8 | last-of-pair << 9 | new-pair-in-range << 10,
 //   w = tiles of the sequences before s (the pair's place in the batch's tile order).
+// With a window z also holds which rows of the tile are hidden, those from row (z >> 16) & 31 (the
+// sinks' end) up to row (z >> 24) & 31 (the window's start), none when the first is not below.
 constexpr int F_FIRST = 1 << 8, F_LAST = 1 << 9, F_NEWPAIR = 1 << 10;
 
-template <typename T, int D, int S, int NW, int NB>
+// WIN: a sliding window with sinks (a.window > 0); only the tiles that hold a visible key are laid
+// out, and the hidden rows of the two tiles at its edges are masked like the rows past the end.
+template <typename T, int D, int S, int NW, int NB, bool WIN>
 __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                                                             const __grid_constant__ CUtensorMap tmv,
                                                             const DecodeArgs a) {
@@ -560,7 +590,7 @@ __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constan
   int total, cq;
   int4 w0;
   if (a.self_plan) {
-    self_plan<NW>(a, s_start, s_q, &s_total);
+    self_plan<NW, WIN>(a, s_start, s_q, &s_total);
     init_barriers();  // after the plan's loads, which need no barrier
     total = s_total;
     w0 = s_start[warp];
@@ -581,7 +611,7 @@ __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constan
   // ---- tile walk state: (sequence, KV head, tile within pair, tiles of the pair, tiles before
   // the sequence)
   int cs = w0.x, ch = w0.y, cj = w0.z, cn = w0.w;
-  auto tiles_of = [&](int s) { return (clamped_len(a, s, false) + TILE - 1) / TILE; };
+  auto tiles_of = [&](int s) { return seq_tiles<WIN>(a, s, false); };
 
   // Fill descriptors for range tiles [t0, t0 + 32) into ring slots (t & 63).
   auto fill = [&](int t0) {
@@ -597,10 +627,17 @@ __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constan
     }
     const int t = t0 + lane;
     if (t < n_my) {
-      const int tok0 = jj * TILE;
+      WinTiles wt;
+      Span sp{0, 0};
+      if constexpr (WIN) {
+        wt = win_tiles(a, ss, false);
+        sp.len = wt.len;
+      } else {
+        sp = seq_span(a, ss, false);
+      }
+      const int tok0 = WIN ? wt.token0(jj) : jj * TILE;
       const int lb = tok0 / a.B;
       const int sub = tok0 - lb * a.B;
-      const Span sp = seq_span(a, ss, false);
       int blk = a.tables[static_cast<int64_t>(ss) * a.W + sp.kb + lb];
       if (blk < 0 || blk >= a.num_blocks) {
         record_error(a.err, DERR_DECODE_BLOCK, blk);
@@ -611,6 +648,8 @@ __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constan
       if (jj == 0) flags |= F_FIRST;
       if (jj == nn - 1) flags |= F_LAST;
       if (jj == 0 || t == 0) flags |= F_NEWPAIR;
+      if constexpr (WIN)
+        flags |= max(0, min(TILE, wt.ns - tok0)) << 16 | max(0, min(TILE, wt.lo - tok0)) << 24;
       const int row = ((blk * a.L + a.layer) * a.H_kv + hh) * a.B + sub;
       desc[t & 63] = make_int4(row, ss * a.H_kv + hh, flags, qq);
     }
@@ -766,7 +805,24 @@ __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constan
 #pragma unroll
       for (int r = 0; r < 4; ++r) sc[nb][r] = (sa[nb][r] + sb[nb][r]) * a.scale_log2;
     const int valid = d.z & 0xff;
-    if (valid < TILE) {
+    if constexpr (WIN) {
+      const int hid0 = (d.z >> 16) & 31, hid1 = (d.z >> 24) & 31;  // rows the window hides
+      if (valid < TILE || hid0 < hid1) {
+        auto hidden = [&](int r) { return r >= valid || (r >= hid0 && r < hid1); };
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (hidden(trow)) sc[nb][0] = sc[nb][1] = -INFINITY;
+          if (hidden(trow + 8)) sc[nb][2] = sc[nb][3] = -INFINITY;
+        }
+        // zero the hidden V rows so that 0 * (whatever lies there) cannot make NaN
+        uint8_t* vrows = region + st * C::STAGE_BYTES + C::KV_TILE_BYTES;
+        for (int k = lane; k < TILE * 8 * C::NBOX; k += 32)
+          if (hidden(k / 8 % TILE))
+            *reinterpret_cast<int4*>(vrows + k / (8 * TILE) * (TILE * 128) + k / 8 % TILE * 128 + k % 8 * 16) =
+                make_int4(0, 0, 0, 0);
+        __syncwarp();
+      }
+    } else if (valid < TILE) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         if (trow >= valid) sc[nb][0] = sc[nb][1] = -INFINITY;
@@ -935,6 +991,9 @@ __global__ void __launch_bounds__(NW * 32) decode_tc_kernel(const __grid_constan
         const unsigned long long prev = atomicCAS(c, cur, ours ? cur + 1 : ((a.epoch << 16) | 1ull));
         if (prev == cur) {
           last = (ours ? static_cast<int>(cur & 0xffffull) : 0) == wb - wa;
+          // nobody else counts here any more: cleared, so that a captured launch, whose tag is the
+          // same at every replay, counts from zero again
+          if (last) atomicExch(c, 0ull);
           break;
         }
         cur = prev;
@@ -967,8 +1026,8 @@ __global__ void __launch_bounds__(SIMT_WARPS * 32) decode_simt_kernel(const Deco
     len = len < 0 ? 0 : static_cast<int>(maxlen);
   }
   const int64_t row = (static_cast<int64_t>(s) * a.H_q + g * a.G) * d;
-  simt_attend<TS, TA, NPL, HP>(a, kp, vp, d, s, g, len, static_cast<const TA*>(a.q) + row,
-                               static_cast<TA*>(a.out) + row);
+  simt_attend<TS, TA, NPL, HP>(a, kp, vp, d, s, g, len, visible_at(a.window, a.n_sink, len - 1),
+                               static_cast<const TA*>(a.q) + row, static_cast<TA*>(a.out) + row);
 }
 
 // --------------------------------------------------------------------------- host side
@@ -1015,9 +1074,9 @@ int device_sm_count(int* n) {
   return PKV_OK;
 }
 
-template <typename T, int D, int S, int NW, int NB = 1>
+template <typename T, int D, int S, int NW, int NB = 1, bool WIN = false>
 const void* tc_kernel_ptr() {
-  return reinterpret_cast<const void*>(&decode_tc_kernel<T, D, S, NW, NB>);
+  return reinterpret_cast<const void*>(&decode_tc_kernel<T, D, S, NW, NB, WIN>);
 }
 
 using KernelPtr = const void*;
@@ -1066,9 +1125,33 @@ KernelPtr tc_kernel_with(const Pool& P, const TcVariant& v, int* smem) {
 
 KernelPtr tc_kernel_for(const Pool& P, int* smem) { return tc_kernel_with(P, tc_variant(P), smem); }
 
-// Persistent grid for the tensor-core kernel: resident CTAs per SM x SM count.
-int tc_grid(const Pool& P, int* grid, int* warps, int* smem) {
-  KernelPtr k = tc_kernel_for(P, smem);
+// The windowed form of the kernel, with its stages and warps.
+template <typename T, int D>
+KernelPtr pick_win(int G, int* warps, int* smem) {
+  constexpr int EB = std::is_same<T, E4M3>::value ? 1 : 2;
+  if (G > GPAD) {
+    *warps = 4;
+    *smem = TcSmem<D, EB, 2, 4, 2>::TOTAL;
+    return tc_kernel_ptr<T, D, 2, 4, 2, true>();
+  }
+  constexpr int NW = EB == 1 ? 2 : 4;
+  *warps = NW;
+  *smem = TcSmem<D, EB, 2, NW>::TOTAL;
+  return tc_kernel_ptr<T, D, 2, NW, 1, true>();
+}
+KernelPtr win_kernel_for(const Pool& P, int* warps, int* smem) {
+  const int G = P.geo.H_q / P.geo.H_kv;
+  if (P.geo.dtype == PKV_E4M3) return pick_win<E4M3, 128>(G, warps, smem);
+  const bool bf = P.geo.dtype == PKV_BF16;
+  if (P.geo.d_head == 128)
+    return bf ? pick_win<__nv_bfloat16, 128>(G, warps, smem) : pick_win<__half, 128>(G, warps, smem);
+  return bf ? pick_win<__nv_bfloat16, 64>(G, warps, smem) : pick_win<__half, 64>(G, warps, smem);
+}
+
+// Persistent grid for the tensor-core kernel (or its windowed form): resident CTAs per SM x SM count.
+int tc_grid(const Pool& P, int* grid, int* warps, int* smem, bool win = false) {
+  int nw = tc_variant(P).warps;
+  KernelPtr k = win ? win_kernel_for(P, &nw, smem) : tc_kernel_for(P, smem);
   int dev = 0;
   cudaGetDevice(&dev);
   struct Known {
@@ -1083,14 +1166,13 @@ int tc_grid(const Pool& P, int* grid, int* warps, int* smem) {
     for (const auto& kn : known)
       if (kn.dev == dev && kn.k == k) {
         *grid = kn.grid;
-        *warps = tc_variant(P).warps;
+        *warps = nw;
         return PKV_OK;
       }
   }
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, *smem);
   if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
   int per_sm = 0;
-  const int nw = tc_variant(P).warps;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, nw * 32, *smem);
   if (e != cudaSuccess || per_sm < 1)
     return fail(PKV_ERR_CUDA, std::string("occupancy query: ") + cudaGetErrorString(e));
@@ -1272,7 +1354,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // scale is folded into the softmax scale and the value scale into the final
 // normalisation (stored code * scale is the element's value).
 int fill_args(const Pool& P, int32_t layer, const void* q, void* out, const int32_t* tables, int32_t W,
-              const int32_t* seq_lens, int32_t n_seq, float scale, DecodeArgs* a) {
+              const int32_t* seq_lens, int32_t n_seq, float scale, const Window& win, DecodeArgs* a) {
   const auto& g = P.geo;
   void* err = nullptr;
   if (int rc = device_error_word(&err)) return rc;
@@ -1296,6 +1378,8 @@ int fill_args(const Pool& P, int32_t layer, const void* q, void* out, const int3
   const bool fp8 = g.dtype == PKV_E4M3;
   a->scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (fp8 ? P.k_scale : 1.0));
   a->v_mul = fp8 ? P.v_scale : 1.f;
+  a->window = win.size;
+  a->n_sink = win.sinks;
   return PKV_OK;
 }
 
@@ -1348,7 +1432,9 @@ int decode_workspace_bytes(const Pool& P, int32_t n_seq, size_t* bytes) {
   if (tc_eligible(P)) {
     int grid = 0, nw = 0, smem = 0;
     if (int rc = tc_grid(P, &grid, &nw, &smem)) return rc;
-    warps_total = static_cast<int64_t>(grid) * nw;
+    int win_grid = 0, win_nw = 0;
+    if (int rc = tc_grid(P, &win_grid, &win_nw, &smem, true)) return rc;
+    warps_total = std::max(static_cast<int64_t>(grid) * nw, static_cast<int64_t>(win_grid) * win_nw);
   }
   *bytes = ws_layout(n_seq, P.geo.H_kv, warps_total, P.geo.d_head, P.geo.H_q / P.geo.H_kv, share_slots(P, n_seq))
                .total;
@@ -1358,7 +1444,7 @@ int decode_workspace_bytes(const Pool& P, int32_t n_seq, size_t* bytes) {
 int launch_decode(Pool& P, int32_t layer, const void* q, const void* k_pool, const void* v_pool,
                   const int32_t* tables, int32_t W, const int32_t* seq_lens, int32_t n_seq, float scale, void* out,
                   void* ws, size_t ws_bytes, void* stream, const AppendFuse* fuse, const ShareLaunch* share,
-                  bool long_batch) {
+                  bool long_batch, const Window& win) {
   const auto& g = P.geo;
   const int G = g.H_q / g.H_kv;
   if (G > SIMT_GMAX || (G > GPAD && g.d_head > 128))
@@ -1369,13 +1455,14 @@ int launch_decode(Pool& P, int32_t layer, const void* q, const void* k_pool, con
     return fail(PKV_ERR_INVALID_ARG, "batch too large (tile count must stay below 2^31)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DecodeArgs a;
-  if (int rc = fill_args(P, layer, q, out, tables, W, seq_lens, n_seq, scale, &a)) return rc;
+  if (int rc = fill_args(P, layer, q, out, tables, W, seq_lens, n_seq, scale, win, &a)) return rc;
 
   if (tc_eligible(P)) {
     int grid = 0, nw = 0, smem = 0;
-    if (int rc = tc_grid(P, &grid, &nw, &smem)) return rc;
+    const bool windowed = win.size > 0;
+    if (int rc = tc_grid(P, &grid, &nw, &smem, windowed)) return rc;
     const bool shared = share && share->n_items > 0;
-    KernelPtr kern = tc_kernel_for(P, &smem);
+    KernelPtr kern = windowed ? win_kernel_for(P, &nw, &smem) : tc_kernel_for(P, &smem);
     if (shared && share->decode_sms > 0 && G <= GPAD) {
       // beside the prefix kernel: one 8-warp CTA on each of decode_sms SMs, its dynamic shared
       // memory raised so that no SM takes two (the prefix kernel's CTAs take the other SMs)
@@ -1528,7 +1615,7 @@ extern "C" int pkv_decode_attention_noalloc(const pkv_pool* pool, int32_t layer,
     return fail(PKV_ERR_INVALID_ARG, "batch too large (tile count must stay below 2^31)");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   DecodeArgs a;
-  if (int rc = fill_args(P, layer, q, out, block_tables, W, seq_lens, n_seq, scale, &a)) return rc;
+  if (int rc = fill_args(P, layer, q, out, block_tables, W, seq_lens, n_seq, scale, Window(), &a)) return rc;
 
   if (!tc_eligible(P)) {
     // the CUDA-core kernel needs no scratch at all

@@ -153,15 +153,20 @@ struct AppendFuse {
   void* k_pool;
   void* v_pool;
 };
+// A sliding window over the keys (size 0: every key is visible): a query at position p sees
+// t <= p with t > p - size or t < sinks.
+struct Window {
+  int32_t size = 0, sinks = 0;
+};
 // long_batch: the caller knows (from the lengths on the host) that the batch averages at least
 // 1,024 tiles per (sequence, KV head) pair; such a batch streams faster from a smaller grid.
 int launch_decode(Pool& P, int32_t layer, const void* q, const void* k_pool, const void* v_pool,
                   const int32_t* tables, int32_t W, const int32_t* seq_lens, int32_t n_seq, float scale, void* out,
                   void* ws, size_t ws_bytes, void* stream, const AppendFuse* fuse = nullptr,
-                  const ShareLaunch* share = nullptr, bool long_batch = false);
+                  const ShareLaunch* share = nullptr, bool long_batch = false, const Window& win = Window());
 int launch_prefill(Pool& P, int32_t layer, const void* q, const int32_t* q_off, int32_t n_tok, int32_t max_q,
                    const void* k_pool, const void* v_pool, const int32_t* tables, int32_t W, const int32_t* seq_lens,
-                   int32_t n_seq, float scale, void* out, void* stream);
+                   int32_t n_seq, float scale, void* out, void* stream, const Window& win = Window());
 void destroy_tensor_maps(Pool& P);
 
 // Device error codes recorded by kernels (the `code` of pkv_check_device_error).
