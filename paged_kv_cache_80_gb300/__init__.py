@@ -235,6 +235,12 @@ class Pool:
         self._meta_ints = {}  # (n, W) -> step metadata int32 count (cleared when sharing changes)
         g = geometry
         self._kv_elems = g.num_blocks * g.L * g.H_kv * g.block_size * g.d_head  # elements of k_pool (or v_pool)
+        self._dims = (g.dtype, g.H_q, g.H_kv, g.d_head)
+        self._act_types = None  # torch dtypes of activations, from the first call that needs them on
+
+    def _resolve_types(self):
+        self._act_types = (_types(self.geometry.dtype)[0],)
+        return self._act_types
 
     @property
     def _as_parameter_(self):
@@ -441,55 +447,88 @@ def pkv_append_kv(pool: PoolLike, layer: int, k_new, v_new, slot_mapping, k_pool
                               _dev(v_pool, "v_pool"), _stream(stream)), "pkv_append_kv")
 
 
+# The calls below check type, device, shape and strides of every tensor, since the library sees
+# pointers alone.  A call that launches one kernel takes about 10 us of host time, so the checks go
+# the shortest way through torch: each helper tests what has to hold at once and asks what was
+# wrong (_reject) only when something was.
 _TORCH_TYPES = {}  # pool dtype -> (activation dtype, dtypes a pool tensor may have); filled at the first use
+_torch = None      # the torch module, from the same time on
+_raw_stream = None  # device index -> handle of its current stream
 
 
-def _types(dtype: int):
-    if not _TORCH_TYPES:
-        import torch
+def _init_torch():
+    global _torch, _raw_stream
+    import torch
 
-        f8 = (torch.uint8, torch.float8_e4m3fn)
-        _TORCH_TYPES.update({F32: (torch.float32, (torch.float32,)), F16: (torch.float16, (torch.float16,)),
-                             BF16: (torch.bfloat16, (torch.bfloat16,)), E4M3: (torch.bfloat16, f8), "i32": torch.int32})
+    f8 = (torch.uint8, torch.float8_e4m3fn)
+    _TORCH_TYPES.update({F32: (torch.float32, (torch.float32,)), F16: (torch.float16, (torch.float16,)),
+                         BF16: (torch.bfloat16, (torch.bfloat16,)), E4M3: (torch.bfloat16, f8),
+                         "i32": (torch.int32, (torch.int32,))})
+    # a third of the time of torch.cuda.current_stream(), which makes a Stream object
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+
+
+def _types(dtype):
+    if _torch is None:
+        _init_torch()
     return _TORCH_TYPES[dtype]
 
 
 def _current_device() -> int:
-    import torch
+    if _torch is None:
+        _init_torch()
+    return _torch.cuda.current_device()
 
-    return torch.cuda.current_device()
+
+def _stream_on(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None else _stream(stream)
 
 
-def _dev_as(t, what: str, dtypes, device: int) -> int:
-    """Device pointer of a contiguous CUDA tensor of one of dtypes on the current device."""
-    p = _dev(t, what)
+def _reject(t, what: str, dtypes, device: int, shape=None):
+    """Raise for the first thing wrong with a tensor argument."""
+    if not hasattr(t, "is_cuda") or not t.is_cuda:
+        raise TypeError(f"{what} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{what} is {t.dtype}, not {' or '.join(str(x) for x in dtypes)}")
     if t.get_device() != device:
         raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{device}")
-    return p
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _dev_as(t, what: str, dtypes, device: int, shape=None) -> int:
+    """Device pointer of a contiguous CUDA tensor of one of dtypes on the current device."""
+    try:
+        if t.get_device() == device and t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _reject(t, what, dtypes, device, shape)
 
 
 def _pools(pool: Pool, k_pool, v_pool, device: int):
     """Pointers of the two pool tensors (their type, device and size checked)."""
     dtypes = _types(pool.geometry.dtype)[1]
     k, v = _dev_as(k_pool, "k_pool", dtypes, device), _dev_as(v_pool, "v_pool", dtypes, device)
+    need = pool._kv_elems
     for t, what in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if t.numel() < pool._kv_elems:
-            raise ValueError(f"{what} holds {t.numel()} elements; the pool has {pool._kv_elems}")
+        if t.numel() < need:
+            raise ValueError(f"{what} holds {t.numel()} elements; the pool has {need}")
     return k, v
 
 
-def _rows(t, what: str, n: int, heads: int, d: int, dtype, device: int):
+def _rows(t, what: str, shape, dtypes, device: int):
     """(pointer, elements between rows) of [n][heads][d] rows whose heads lie side by side."""
-    if not hasattr(t, "is_cuda") or not t.is_cuda:
-        raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} is {t.dtype}, not {dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{what} is on cuda:{t.get_device()}, the current device is cuda:{device}")
-    if tuple(t.shape) != (n, heads, d):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(n, heads, d)}")
+    try:
+        fits = t.get_device() == device and t.dtype in dtypes and t.shape == shape
+    except AttributeError:
+        fits = False
+    if not fits:
+        _reject(t, what, dtypes, device, shape)
+    n, heads, d = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
@@ -526,25 +565,31 @@ def pkv_append_kv_rotary(pool: Pool, layer: int, rotary: Rotary, q, k_new, v_new
     and the values at their slots.  q, q_out [n][H_q][d], k_new, v_new [n][H_kv][d]: rows may be
     strided (parts of a fused projection); positions int32 [n_axes][n] ([n] with one axis); q and
     q_out None: keys and values only."""
-    g = pool.geometry
+    L = _lib or _L()
     dev = _current_device()
-    act, i32 = _types(g.dtype)[0], (_types("i32"),)
+    dtype, H_q, H_kv, d = pool._dims
+    act, i32 = pool._act_types or pool._resolve_types(), _TORCH_TYPES["i32"][1]
     n = slot_mapping.numel()
-    if positions.numel() != rotary.n_axes * n or (positions.dim() != 2 and rotary.n_axes > 1):
+    if positions.numel() != rotary.n_axes * n or (rotary.n_axes > 1 and positions.dim() != 2):
         raise ValueError(f"positions has shape {tuple(positions.shape)}, not {(rotary.n_axes, n)}")
     if rotary.inv_freq.get_device() != dev:
         raise ValueError(f"inv_freq is on cuda:{rotary.inv_freq.get_device()}, the current device is cuda:{dev}")
-    qp = qs = op = os_ = None
+    qp = op = None
+    qs = os_ = 0
     if q is not None or q_out is not None:
-        qp, qs = _rows(q, "q", n, g.H_q, g.d_head, act, dev)
-        op, os_ = _rows(q_out, "q_out", n, g.H_q, g.d_head, act, dev)
-    kn, ks = _rows(k_new, "k_new", n, g.H_kv, g.d_head, act, dev)
-    vn, vs = _rows(v_new, "v_new", n, g.H_kv, g.d_head, act, dev)
+        shape = (n, H_q, d)
+        qp, qs = _rows(q, "q", shape, act, dev)
+        op, os_ = _rows(q_out, "q_out", shape, act, dev)
+    shape = (n, H_kv, d)
+    kn, ks = _rows(k_new, "k_new", shape, act, dev)
+    vn, vs = _rows(v_new, "v_new", shape, act, dev)
     kp, vp = _pools(pool, k_pool, v_pool, dev)
-    _check(_L().pkv_append_kv_rotary(pool.handle, layer, rotary._addr, qp, qs or 0, kn, ks, vn, vs,
-                                     _dev_as(positions, "positions", i32, dev),
-                                     _dev_as(slot_mapping, "slot_mapping", i32, dev), n, op, os_ or 0, kp, vp,
-                                     _stream(stream)), "pkv_append_kv_rotary")
+    rc = L.pkv_append_kv_rotary(pool.handle, layer, rotary._addr, qp, qs, kn, ks, vn, vs,
+                                _dev_as(positions, "positions", i32, dev),
+                                _dev_as(slot_mapping, "slot_mapping", i32, dev), n, op, os_, kp, vp,
+                                _stream_on(stream, dev))
+    if rc:
+        _check(rc, "pkv_append_kv_rotary")
 
 
 def pkv_decode_workspace_size(pool: PoolLike, n_seq: int) -> int:
@@ -797,43 +842,50 @@ def pkv_prefill_attention(pool: PoolLike, layer: int, q, q_offsets, max_q: int, 
 def _attention_args(pool: Pool, q, k_pool, v_pool, block_tables, seq_lens, out, rows: int, device: int):
     """Pointers of a windowed attention call's tensors, their types, shapes and device checked:
     (q, k_pool, v_pool, block_tables, W, seq_lens, n_seq, out)."""
-    g = pool.geometry
-    act, i32 = (_types(g.dtype)[0],), (_types("i32"),)
-    qp, op = _dev_as(q, "q", act, device), _dev_as(out, "out", act, device)
-    for t, what in ((q, "q"), (out, "out")):
-        if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != g.H_q or t.shape[2] != g.d_head:
-            raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, g.H_q, g.d_head)}")
+    dtype, H_q, H_kv, d = pool._dims
+    act = pool._act_types or pool._resolve_types()
+    i32 = _TORCH_TYPES["i32"][1]
+    shape = (rows, H_q, d)
+    qp, op = _dev_as(q, "q", act, device, shape), _dev_as(out, "out", act, device, shape)
     kp, vp = _pools(pool, k_pool, v_pool, device)
     tp, lp = _dev_as(block_tables, "block_tables", i32, device), _dev_as(seq_lens, "seq_lens", i32, device)
     n = seq_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != n:
-        raise ValueError(f"block_tables has shape {tuple(block_tables.shape)}, not ({n}, W)")
-    return qp, kp, vp, tp, block_tables.shape[1], lp, n, op
+    ts = block_tables.shape
+    if len(ts) != 2 or ts[0] != n:
+        raise ValueError(f"block_tables has shape {tuple(ts)}, not ({n}, W)")
+    return qp, kp, vp, tp, ts[1], lp, n, op
 
 
 def pkv_decode_attention_window(pool: Pool, layer: int, q, k_pool, v_pool, block_tables, seq_lens, window: int,
                                 n_sink: int, scale: float, out, workspace, stream=None) -> None:
     """pkv_decode_attention over the last `window` keys of each sequence and its first `n_sink`."""
+    L = _lib or _L()
     dev = _current_device()
     qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out,
                                                    seq_lens.numel(), dev)
-    _check(_L().pkv_decode_attention_window(pool.handle, layer, qp, kp, vp, tp, W, lp, n, window, n_sink, scale, op,
-                                            _dev(workspace, "workspace"), _nbytes(workspace), _stream(stream)),
-           "pkv_decode_attention_window")
+    if workspace.get_device() != dev:
+        _reject(workspace, "workspace", (workspace.dtype,), dev)
+    rc = L.pkv_decode_attention_window(pool.handle, layer, qp, kp, vp, tp, W, lp, n, window, n_sink, scale, op,
+                                       _dev(workspace, "workspace"), workspace.nbytes, _stream_on(stream, dev))
+    if rc:
+        _check(rc, "pkv_decode_attention_window")
 
 
 def pkv_prefill_attention_window(pool: Pool, layer: int, q, q_offsets, max_q: int, k_pool, v_pool, block_tables,
                                  seq_lens, window: int, n_sink: int, scale: float, out, stream=None) -> None:
     """pkv_prefill_attention in which the query at position p sees its last `window` keys and the
     sequence's first `n_sink`; rows of q and out past q_offsets[n_seq] are left alone."""
+    L = _lib or _L()
     dev = _current_device()
-    qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, q.shape[0], dev)
-    offs = _dev_as(q_offsets, "q_offsets", (_types("i32"),), dev)
+    n_tok = q.shape[0]
+    qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, n_tok, dev)
+    offs = _dev_as(q_offsets, "q_offsets", _TORCH_TYPES["i32"][1], dev)
     if q_offsets.numel() != n + 1:
         raise ValueError(f"q_offsets has {q_offsets.numel()} entries, not {n + 1}")
-    _check(_L().pkv_prefill_attention_window(pool.handle, layer, qp, offs, q.shape[0], max_q, kp, vp, tp, W, lp, n,
-                                             window, n_sink, scale, op, _stream(stream)),
-           "pkv_prefill_attention_window")
+    rc = L.pkv_prefill_attention_window(pool.handle, layer, qp, offs, n_tok, max_q, kp, vp, tp, W, lp, n, window,
+                                        n_sink, scale, op, _stream_on(stream, dev))
+    if rc:
+        _check(rc, "pkv_prefill_attention_window")
 
 
 def pkv_copy_blocks(pool: PoolLike, pairs, k_pool, v_pool, stream=None) -> None:

@@ -128,11 +128,11 @@ __global__ void __launch_bounds__(256) rotary_append_any_kernel(const __grid_con
 // Rows made of 16-byte vectors (d_head and rotary_dim multiples of 2 E, E elements a vector; every row and
 // pool on a 16-byte boundary).  A thread handles chunk c of a row, two vectors that hold both elements of E
 // pairs: elements E c .. and rotary_dim / 2 + E c .. of a rotated head in halves, 2 E c .. (adjacent pairs), or
-// 2 E neighbours past rotary_dim; c stays the same for all of a thread's rows.  A CTA takes tiles of
-// `tokens` tokens (or, when there are few, one split of one token's rows): its first rows' vectors are on
-// their way while each thread makes the cosines and sines of one frequency, which all H_q + H_kv heads of a
+// 2 E neighbours past rotary_dim; c stays the same for all of a thread's rows.  A CTA takes
+// its tokens (or, when there are few, one of `splits` parts of one token's rows): the first rows' vectors are
+// on their way while each thread makes the cosines and sines of one frequency, which all H_q + H_kv heads of a
 // token share through shared memory, as float4 entries [token][E / 2][chunk] that neighbouring threads read
-// without bank conflicts.  The work is the bytes moved: everything else has to hide behind them.
+// without bank conflicts.  A CTA's tokens are a range of its own, taken `tokens` at a time.  The work is the bytes moved: everything else has to hide behind them.
 template <typename TA>
 struct RowVec {
   static constexpr int E = 16 / sizeof(TA);
@@ -162,9 +162,10 @@ __device__ __forceinline__ uint2 codes_of(const float (&f)[8], float scale) {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotUnroll = 2;  // rows a thread has in flight
+constexpr int kRotCtas = 4;    // resident CTAs an SM the registers have to allow
 
 template <typename TA, bool F8, bool INTER>
-__global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const __grid_constant__ RotaryArgs a, int tokens,
+__global__ void __launch_bounds__(kRotThreads, kRotCtas) rotary_append_kernel(const __grid_constant__ RotaryArgs a, int tokens,
                                                                      int splits) {
   using RV = RowVec<TA>;
   constexpr int E = RV::E, U = kRotUnroll;
@@ -180,13 +181,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const __grid
   unsigned long long u = 0;
   const int32_t* pos = a.positions + static_cast<int64_t>(a.axis[fi]) * a.n_tok;
   float2* cs_out = reinterpret_cast<float2*>(cs4) + (((fi % E) / 2) * nch + fi / E) * 2 + (fi & 1);
-  const int tiles = (a.n_tok + tokens - 1) / tokens;
+  const int groups = gridDim.x / splits, group = blockIdx.x / splits, sp = blockIdx.x - group * splits;
+  const int rb = first_row + sp * per, nr = min(all_rows, rb + per) - rb;  // this split's rows
+  const int64_t t_end = static_cast<int64_t>(a.n_tok) * (group + 1) / groups;
   bool first = true;
-  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(tiles) * splits; w += gridDim.x) {
-    const int tile = static_cast<int>(w / splits), sp = static_cast<int>(w - static_cast<int64_t>(tile) * splits);
-    const int64_t t0 = static_cast<int64_t>(tile) * tokens;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), a.n_tok - t0));
-    const int rb = first_row + sp * per, nr = min(all_rows, rb + per) - rb;  // this split's rows
+  for (int64_t t0 = static_cast<int64_t>(a.n_tok) * group / groups; t0 < t_end; t0 += tokens) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), t_end - t0));
     int t = 0, row = r0;  // the next row to load: token t of the tile, row rb + row
     auto settle = [&] {
       while (row >= nr && t < nt) {
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const __grid
     if (r0 >= rpp || nr <= 0) t = nt;
     settle();
     uint4 x0[U], x1[U];
-    int xt[U], xr[U];
+    int xt[U], xr[U], xs[U];
     auto load = [&](int k) {
       xt[k] = t;
       xr[k] = rb + row;
@@ -210,16 +210,21 @@ __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const __grid
                           : static_cast<const TA*>(a.v) + tok * a.v_stride + static_cast<int64_t>(r - a.H_q - a.H_kv) * a.d;
       x0[k] = *reinterpret_cast<const uint4*>(src + o0);
       x1[k] = *reinterpret_cast<const uint4*>(src + o1);
+      if (r >= a.H_q) xs[k] = a.slots[tok];
       row += rpp;
       settle();
     };
 #pragma unroll
     for (int k = 0; k < U; ++k) load(k);
+    int32_t p = ft < nt ? pos[t0 + ft] : 0;
     if (first) u = turns_of(a.inv_freq[fi]);
     else __syncthreads();  // every thread is done with the last tile's angles
     first = false;
     if (ft < tpp)
-      for (int k = ft; k < nt; k += tpp) cs_out[static_cast<int64_t>(k) * half] = cos_sin(u, pos[t0 + k]);
+      for (int k = ft; k < nt; k += tpp) {
+        cs_out[k * half] = cos_sin(u, p);
+        if (k + tpp < nt) p = pos[t0 + k + tpp];
+      }
     __syncthreads();
     while (xt[0] < nt) {
 #pragma unroll
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const __grid
           *reinterpret_cast<uint4*>(dst + o0) = RV::pack(f0);
           *reinterpret_cast<uint4*>(dst + o1) = RV::pack(f1);
         } else {
-          const int32_t slot = a.slots[tok];
+          const int32_t slot = xs[k];
           const int h = is_v ? r - a.H_q - a.H_kv : r - a.H_q;
           if (slot < 0 || slot >= a.n_slots) {
             if (c == 0 && h == 0 && !is_v) record_error(a.err, DERR_APPEND_SLOT, slot);
@@ -314,16 +319,15 @@ void launch_t(const RotaryArgs& a, cudaStream_t st) {
     rotary_append_any_kernel<TA, F8, INTER><<<grid, 256, 0, st>>>(a);
     return;
   }
-  // Few tokens: each thread one row, a token's rows over several CTAs.  Otherwise tiles of up to
-  // kTokens tokens for a grid that stays resident (4 CTAs an SM).
-  constexpr int kTokens = 4;
+  // Few tokens: a token's rows over as many CTAs as one resident wave has room for.  Many: tiles of
+  // kTokens tokens over a resident grid.
+  constexpr int kTokens = 8;
+  const int64_t cap = sms * kRotCtas;
   const int rows = (a.q ? a.H_q : 0) + 2 * a.H_kv, rpp = kRotThreads / (a.d / (2 * E));
   const int64_t passes = (rows + rpp - 1) / rpp;
-  int tokens = 1, splits = 1;
-  if (a.n_tok * passes <= sms * 8) splits = static_cast<int>(passes);
-  else tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTokens, a.n_tok / (sms * 4))));
-  const int64_t work = static_cast<int64_t>((a.n_tok + tokens - 1) / tokens) * splits;
-  const int grid = static_cast<int>(std::min<int64_t>(work, splits > 1 ? sms * 8 : sms * 4));
+  const int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(passes, cap / a.n_tok)));
+  const int groups = static_cast<int>(std::min<int64_t>(a.n_tok, cap / splits));
+  const int tokens = std::min(kTokens, (a.n_tok + groups - 1) / groups), grid = groups * splits;
   const size_t smem = static_cast<size_t>(tokens) * a.rot / 2 * sizeof(float2);
   rotary_append_kernel<TA, F8, INTER><<<grid, kRotThreads, smem, st>>>(a, tokens, splits);
 }
