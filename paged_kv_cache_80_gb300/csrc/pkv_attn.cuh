@@ -266,4 +266,10 @@ int fill_args(const Pool& P, int32_t layer, const void* q, void* out, const int3
 int launch_prefix_share(Pool& P, const DecodeArgs& a, const void* q, const void* k_pool, const void* v_pool,
                         int32_t n_items, int32_t max_members, cudaStream_t st);
 
+// Windowed decode of a small batch, a cluster of CTAs per (sequence, KV head) pair (pkv_window.cu):
+// CTAs per pair, 0 where the persistent kernel is the better one; and the launch.
+int win_cluster_size(int64_t pairs, int64_t tiles, int sms);
+int launch_decode_clusters(const Pool& P, DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int csize,
+                           cudaStream_t st);
+
 }  // namespace pkv

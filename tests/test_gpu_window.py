@@ -242,17 +242,18 @@ def test_offsets_past_32_bits(dtype, d, chunks):
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_a_wide_window_is_the_whole_sequence(dtype):
-    """window >= len: the same keys as the calls without a window, on the same path."""
+    """window >= len: the keys of the calls without a window.  The two may cut a sequence in different places, so that
+    their partial sums are rounded differently: each is held to the definition, not to the other's bits."""
     b = Batch(dtype, LENS, 4096, 0)
     b.call()
-    plain = torch.empty_like(b.out)
-    pkv.pkv_decode_attention(b.pool, 0, b.q, b.kp, b.vp, b.tables, b.lens_d, b.scale, plain, b.ws)
-    assert torch.equal(plain, b.out)
+    b.check()
+    pkv.pkv_decode_attention(b.pool, 0, b.q, b.kp, b.vp, b.tables, b.lens_d, b.scale, b.out.fill_(math.nan), b.ws)
+    b.check()
     p = Batch(dtype, [300, 700], 4096, 0, [300, 77])
     p.call()
-    plain = torch.full_like(p.out, math.nan)
-    pkv.pkv_prefill_attention(p.pool, 0, p.q, p.offs_d, 300, p.kp, p.vp, p.tables, p.lens_d, p.scale, plain)
-    assert torch.equal(plain, p.out)
+    p.check()
+    pkv.pkv_prefill_attention(p.pool, 0, p.q, p.offs_d, 300, p.kp, p.vp, p.tables, p.lens_d, p.scale, p.out.fill_(math.nan))
+    p.check()
 
 
 def test_replayed_graphs_that_share_a_workspace():
