@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libpkv.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["pkv_api.cpp", "pkv_copy.cu", "pkv_decode.cu", "pkv_prefill.cu", "pkv_prefix.cpp", "pkv_rotary.cu",
-           "pkv_sim.cpp", "pkv_window.cu"]
+           "pkv_sim.cpp", "pkv_window.cu", "pkv_window_prefill.cu"]
 HEADERS = ["pkv_internal.h", "pkv_device.cuh", "pkv_attn.cuh", "pkv_tile.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

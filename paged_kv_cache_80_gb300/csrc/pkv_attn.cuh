@@ -271,5 +271,9 @@ int launch_prefix_share(Pool& P, const DecodeArgs& a, const void* q, const void*
 int win_cluster_size(int64_t pairs, int64_t tiles, int sms);
 int launch_decode_clusters(const Pool& P, DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int csize,
                            cudaStream_t st);
+// Windowed chunked prefill on tensor cores (pkv_window_prefill.cu): the geometries it takes; the launch.
+bool win_prefill_ok(const pkv_geometry& g);
+int launch_prefill_window(Pool& P, DecodeArgs& a, const void* q, const int32_t* q_off, int32_t n_tok, int32_t max_q,
+                          const void* k_pool, const void* v_pool, cudaStream_t st);
 
 }  // namespace pkv

@@ -32,35 +32,6 @@ namespace {
 // own pool block, TMA with 128-byte swizzle, two stages).  S = Q K^T and O += P V are
 // mma.sync m16n8k16 with the accumulator of S reused as the A operand of P V.
 
-// With a window: the key tiles (of `keys` keys) that queries at positions pmin .. need.  A key is
-// hidden from all of them if sink_end <= t < lo; tiles 0 .. sink_tiles - 1 hold the sinks, those
-// from `first` on the rest.
-struct WinKeys {
-  int32_t sink_end, lo, sink_tiles, first;
-  __device__ __forceinline__ int32_t tile(int32_t j) const { return j < sink_tiles ? j : first + j - sink_tiles; }
-  __device__ __forceinline__ int32_t count(int32_t nkeys, int keys) const {
-    return sink_tiles + (nkeys + keys - 1) / keys - first;
-  }
-  // all of the keys [t0, t0 + n) hidden from every query: neither read nor looked up
-  __device__ __forceinline__ bool hides(int32_t t0, int32_t n) const { return t0 >= sink_end && t0 + n <= lo; }
-};
-__device__ __forceinline__ WinKeys win_keys(const DecodeArgs& a, int32_t pmin, int keys) {
-  const Visible v = visible_at(a.window, a.n_sink, pmin);
-  WinKeys w;
-  w.sink_end = v.ns;
-  w.lo = v.lo;
-  w.sink_tiles = (v.ns + keys - 1) / keys;
-  w.first = max(w.sink_tiles, v.lo / keys);
-  return w;
-}
-
-// Rows [q_off[s], q_off[s + 1]) of the chunk of sequence s lie in q and out (else recorded).
-__device__ __forceinline__ bool chunk_rows_ok(const DecodeArgs& a, int qbeg, int Cs, int s, bool record) {
-  if (qbeg >= 0 && Cs >= 0 && Cs <= a.n_tok - qbeg) return true;
-  if (record) record_error(a.err, DERR_PREFILL_CHUNK, s);
-  return false;
-}
-
 constexpr int PF_WARPS = 8;
 constexpr int PF_ROWS = PF_WARPS * 16;
 constexpr int PF_KEYS = 64;
@@ -75,7 +46,7 @@ struct PfCfg {
   static constexpr int NBOX = D / 64;
 };
 
-template <typename T, int D, bool WIN>
+template <typename T, int D>
 __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                                                                        const __grid_constant__ CUtensorMap tmv,
                                                                        const DecodeArgs a, const int32_t* q_off,
@@ -90,7 +61,6 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
   const int qbeg = q_off[s];
   const int Cs = q_off[s + 1] - qbeg;
   const int i0 = qb * QB;
-  if (!chunk_rows_ok(a, qbeg, Cs, s, tid == 0 && g == 0)) return;
   if (qb == gridDim.x - 1 && tid == 0 && g == 0 && Cs > i0 + QB) record_error(a.err, DERR_PREFILL_CHUNK, s);
   if (i0 >= Cs) return;  // uniform over the CTA
   const int i1 = min(Cs, i0 + QB);
@@ -102,9 +72,7 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
   const int P = len - Cs;
   const int pmin = P + i0, pmax = P + i1 - 1;
   const int nkeys = pmax + 1;
-  const WinKeys wk = WIN ? win_keys(a, pmin, PF_KEYS) : WinKeys{};
-  const int ntiles = WIN ? wk.count(nkeys, PF_KEYS) : (nkeys + PF_KEYS - 1) / PF_KEYS;
-  auto key0 = [&](int j) { return (WIN ? wk.tile(j) : j) * PF_KEYS; };  // first key of the j-th tile
+  const int ntiles = (nkeys + PF_KEYS - 1) / PF_KEYS;
   const int nblk = (nkeys + a.B - 1) / a.B;
   if (nblk > blk_cap) {  // the host sizes blk_cap from W: cannot happen for valid lengths
     if (tid == 0) record_error(a.err, DERR_DECODE_LEN, s);
@@ -117,7 +85,6 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
   const uint32_t bar0 = smem_u32(base + 2 * C::STAGE + ((blk_cap * 4 + 15) / 16) * 16);
 
   for (int k = tid; k < nblk; k += blockDim.x) {
-    if (WIN && wk.hides(k * a.B, a.B)) continue;
     int b = a.tables[static_cast<int64_t>(s) * a.W + k];
     if (b < 0 || b >= a.num_blocks) {
       record_error(a.err, DERR_DECODE_BLOCK, b);
@@ -136,14 +103,12 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
     const int st = kt & 1;
     const uint32_t bar = bar0 + 8 * st;
     const uint32_t sk = stage0 + st * C::STAGE;
-    auto wanted = [&](int t0) { return t0 < nkeys && !(WIN && wk.hides(t0, TILE)); };
     int n = 0;
-    for (int j = 0; j < PF_SLABS; ++j) n += wanted(key0(kt) + j * TILE) ? 1 : 0;
+    for (int j = 0; j < PF_SLABS; ++j) n += (kt * PF_KEYS + j * TILE < nkeys) ? 1 : 0;
     fence_proxy_async();
     mbar_arrive_expect_tx(bar, 2 * n * C::SLAB);
-    for (int j = 0; j < PF_SLABS; ++j) {
-      const int t0 = key0(kt) + j * TILE;
-      if (!wanted(t0)) continue;
+    for (int j = 0; j < n; ++j) {
+      const int t0 = kt * PF_KEYS + j * TILE;
       const int lb = t0 / a.B;
       const int row = ((blks[lb] * a.L + a.layer) * a.H_kv + g) * a.B + (t0 - lb * a.B);
 #pragma unroll
@@ -163,8 +128,6 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
   const int qi0 = i0 + r0 / G, qi1 = i0 + r1 / G;
   const bool v0 = r0 < QB * G && qi0 < i1, v1 = r1 < QB * G && qi1 < i1;
   const int p0 = v0 ? P + qi0 : pmax, p1 = v1 ? P + qi1 : pmax;  // last visible key
-  const int lo0 = WIN ? visible_at(a.window, a.n_sink, p0).lo : 0, lo1 = WIN ? visible_at(a.window, a.n_sink, p1).lo : 0;
-  const int lo_max = WIN ? visible_at(a.window, a.n_sink, pmax).lo : 0;
   const int64_t qrow0 = (static_cast<int64_t>(qbeg + qi0) * a.H_q + g * G + r0 % G) * D;
   const int64_t qrow1 = (static_cast<int64_t>(qbeg + qi1) * a.H_q + g * G + r1 % G) * D;
   const int c2 = 2 * (lane & 3);
@@ -194,7 +157,7 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
       if (tid == 0 && kt + 1 < ntiles) mbar_wait_bounded(bar0 + 8 * ((kt + 1) & 1), ((kt + 1) >> 1) & 1, kWaitNs);
       return;
     }
-    const int kbase = key0(kt);
+    const int kbase = kt * PF_KEYS;
     const int nvalid = min(PF_KEYS, nkeys - kbase);  // keys of this tile that exist
     if (nvalid < PF_KEYS && (nvalid & (TILE - 1))) {
       // zero the V rows past the last key of the last loaded slab (0 * stale could be NaN)
@@ -204,17 +167,6 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
         const int b = k / ((TILE - r_from) * 8);
         const int rem = k - b * (TILE - r_from) * 8;
         *reinterpret_cast<int4*>(vrows + b * (TILE * 128) + (r_from + rem / 8) * 128 + (rem & 7) * 16) =
-            make_int4(0, 0, 0, 0);
-      }
-      __syncthreads();
-    }
-    if (WIN && max(kbase, wk.sink_end) < min(kbase + PF_KEYS, wk.lo)) {
-      // and the V rows that the window hides from every query of the CTA, whatever lies there
-      uint8_t* vt = base + st * C::STAGE + PF_SLABS * C::SLAB;
-      const int h0 = max(wk.sink_end - kbase, 0), h1 = min(wk.lo - kbase, nvalid);
-      for (int k = tid; k < (h1 - h0) * 8 * C::NBOX; k += blockDim.x) {
-        const int r = h0 + k / (8 * C::NBOX), x = k % (8 * C::NBOX);
-        *reinterpret_cast<int4*>(vt + r / TILE * C::SLAB + x / 8 * (TILE * 128) + r % TILE * 128 + x % 8 * 16) =
             make_int4(0, 0, 0, 0);
       }
       __syncthreads();
@@ -238,9 +190,8 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
       }
     }
     // ---- scale, causal mask, online softmax (rows r0: c0/c1, r1: c2/c3)
-    const bool need_mask = kbase + PF_KEYS - 1 > pmin || (WIN && kbase < lo_max);
+    const bool need_mask = kbase + PF_KEYS - 1 > pmin;
     float x0 = -INFINITY, x1 = -INFINITY;
-    const float mp0 = m0, mp1 = m1;
 #pragma unroll
     for (int grp = 0; grp < PF_KEYS / 8; ++grp) {
 #pragma unroll
@@ -249,7 +200,6 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
         if (need_mask) {
           const int t = kbase + grp * 8 + c2 + (e & 1);
           if (t > ((e < 2) ? p0 : p1)) v = -INFINITY;
-          if (WIN && t < ((e < 2) ? lo0 : lo1) && t >= a.n_sink) v = -INFINITY;
         }
         sf[grp][e] = v;
       }
@@ -260,11 +210,10 @@ __global__ void __launch_bounds__(PF_WARPS * 32, 1) prefill_tc_kernel(const __gr
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-    // without a window finite: key 0 is visible to every row; with one, a row may have seen no key yet,
-    // and 0 stands in for its maximum (every exponential is then 0)
-    m0 = fmaxf(m0, x0), m1 = fmaxf(m1, x1);
-    const float n0 = WIN && m0 == -INFINITY ? 0.f : m0, n1 = WIN && m1 == -INFINITY ? 0.f : m1;
-    const float cr0 = exp2f(mp0 - n0), cr1 = exp2f(mp1 - n1);
+    const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);  // finite: key 0 is visible to every row
+    const float cr0 = exp2f(m0 - n0), cr1 = exp2f(m1 - n1);
+    m0 = n0;
+    m1 = n1;
     float ps0 = 0.f, ps1 = 0.f;
 #pragma unroll
     for (int grp = 0; grp < PF_KEYS / 8; ++grp) {
@@ -405,7 +354,7 @@ constexpr int UM_FS = 2;                         // E4M3 staging ring depth
 __host__ __device__ constexpr int um_ks(bool kv8) { return kv8 ? 3 : 4; }
 // barriers: q; the K and V rings (at most 4 deep); (S, P, O) per tile and S buffer; vz; two drains;
 // turn per tile; the E4M3 staging rings (full, free); Q converted
-constexpr int UM_BARS = 1 + 4 * 4 + 3 * 4 + 3 + 2 + 2 + 4 * UM_FS + 1;
+constexpr int UM_BARS = 1 + 4 * 4 + 3 * 4 + 1 + 2 + 2 + 4 * UM_FS + 1;
 constexpr int UM_TBL = 4096;  // block-table entries staged in shared memory (65,536 tokens at B = 16)
 constexpr int um_smem(bool kv8) {
   return 1024 + 2 * UM_TILE_BYTES + 2 * um_ks(kv8) * UM_KV_BYTES + (kv8 ? 2 * UM_FS * UM_STG_BYTES : 0) + UM_BARS * 8 +
@@ -433,11 +382,7 @@ __device__ __forceinline__ uint32_t bf16x2_rn_f16x2(uint32_t w) {
 // against all keys of blocks [kb0, kb1) of row rb's table (no causal edge: the prefix precedes
 // every query); the epilogue leaves the partial (m, l, unnormalised O) of each (row, head) in
 // slot slot_base + (row - rb) of a.prior_ml / a.prior_o for the combine kernel.
-// WIN: a sliding window with sinks (a.window > 0).  The CTA walks the key tiles that some query of
-// its two tiles sees; keys hidden from all of them have their V rows zeroed in shared memory, keys
-// hidden from a row are masked in its scores, and a row that has seen no key yet (the window of a
-// later query starts tiles after the first one's) keeps m = -inf with 0 standing in for it.
-template <typename T, bool KV8, bool SH = false, bool WIN = false>
+template <typename T, bool KV8, bool SH = false>
 __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __grid_constant__ CUtensorMap tmq,
                                                                       const __grid_constant__ CUtensorMap tmk,
                                                                       const __grid_constant__ CUtensorMap tmv3,
@@ -455,8 +400,6 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
   const int qbeg = SH ? item[0] : q_off[s];
   const int Cs = SH ? item[1] - item[0] : q_off[s + 1] - qbeg;
   const int i0 = qb * 2 * QB;  // first query of tile A
-  if constexpr (!SH)
-    if (!chunk_rows_ok(a, qbeg, Cs, s, tid == 0 && g == 0)) return;
   if (qb == gridDim.x - 1 && tid == 0 && g == 0 && Cs > i0 + 2 * QB) record_error(a.err, DERR_PREFILL_CHUNK, s);
   if (i0 >= Cs) {  // uniform over the CTA, before any barrier or TMEM use
     if constexpr (SH)
@@ -488,19 +431,8 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
   const int nq = i0 + QB < Cs ? 2 : 1;  // tiles with rows in the chunk
   const int i1 = min(Cs, i0 + nq * QB);
   const int pmax = nkeys - 1;
-  const WinKeys wk = WIN ? win_keys(a, P + i0, UM_KEYS) : WinKeys{};
-  const int nt = WIN ? wk.count(nkeys, UM_KEYS) : (nkeys + UM_KEYS - 1) / UM_KEYS;
-  auto key0 = [&](int j) { return (WIN ? wk.tile(j) : j) * UM_KEYS; };  // first key of the j-th key tile
-  // the last tile has keys past the sequence end
-  const bool tail = nkeys % UM_KEYS != 0;
-  // V rows to zero in the j-th tile: those past the end, and those hidden from every row of the CTA
-  // (in at most two tiles: the last with sinks and the first of the window)
-  auto hidden0 = [&](int j) { return max(wk.sink_end - key0(j), 0); };
-  auto hidden1 = [&](int j) { return min(wk.lo - key0(j), UM_KEYS); };
-  auto window_edge = [&](int j) { return WIN && hidden0(j) < hidden1(j); };
-  auto zeroed = [&](int j) { return (tail && j == nt - 1) || window_edge(j); };
-  // each such tile has a barrier of its own
-  auto vz_of = [&](int j) { return WIN ? (j == nt - 1 ? 2 : (j < wk.sink_tiles ? 0 : 1)) : 2; };
+  const int nt = (nkeys + UM_KEYS - 1) / UM_KEYS;
+  const bool tail = nkeys < nt * UM_KEYS;  // the last tile has keys past the sequence end
 
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t qs = smem_u32(base);
@@ -513,7 +445,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
   const uint32_t v_full = k_empty + 8 * KS, v_empty = v_full + 8 * KS;
   // S, P and O barriers are indexed by 2 X + b: tile X, S buffer b
   const uint32_t s_full = v_empty + 8 * KS, p_full = s_full + 32, o_done = p_full + 32, vz = o_done + 32;
-  const uint32_t drain = vz + 24;  // two barriers: the issuers' last commits after an abort
+  const uint32_t drain = vz + 8;  // two barriers: the issuers' last commits after an abort
   const uint32_t turn = drain + 16;  // per tile: its softmax of the current key tile is done
   const uint32_t sk_full = turn + 16, sv_full = sk_full + 8 * UM_FS;  // E4M3 staging landed
   const uint32_t sk_free = sv_full + 8 * UM_FS, sv_free = sk_free + 8 * UM_FS;  // staging read
@@ -548,7 +480,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
       mbar_init(drain + 8 * x, 1);
       mbar_init(turn + 8 * x, 4);  // one arrival per softmax warp
     }
-    for (int i = 0; i < 3; ++i) mbar_init(vz + 8 * i, 1);
+    mbar_init(vz, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -602,10 +534,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
         return blk;
       };
       if (tbl_in_smem) {  // the sequence's table slice, once (both warps write the same values)
-        for (int k = lane; k < nblk; k += 32) {
-          if (WIN && wk.hides(k * a.B, a.B)) continue;
-          tbl[k] = block_at(k);
-        }
+        for (int k = lane; k < nblk; k += 32) tbl[k] = block_at(k);
         __syncwarp();
       }
       const uint32_t full0 = kw ? k_full : v_full, empty0 = kw ? k_empty : v_empty;
@@ -636,14 +565,13 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
         int issued = 0;
         for (int j = 0; j < nt && ok; ++j) {
           int row = 0;
-          const int t0 = key0(j) + lane * TILE;
-          const bool on = lane < UM_SLABS && t0 < nkeys && !(WIN && wk.hides(t0, TILE));  // this lane's slab is read
-          if (on) {
+          const int t0 = j * UM_KEYS + lane * TILE;
+          if (lane < UM_SLABS && t0 < nkeys) {
             const int lb = t0 / a.B;
             const int blk = tbl_in_smem ? tbl[lb] : block_at(lb);
             row = ((blk * a.L + a.layer) * a.H_kv + g) * a.B + (t0 - lb * a.B);
           }
-          const int nv = __popc(__ballot_sync(0xffffffffu, on));
+          const int nv = min(UM_SLABS, (nkeys - j * UM_KEYS + TILE - 1) / TILE);
           const int f = j % UM_FS;
           if (lane == 0) {
             if (j >= UM_FS) ok = wait(sfree0 + 8 * f, ((j / UM_FS) - 1) & 1, 110 + j);
@@ -652,7 +580,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;  // also orders the expect_tx before the copies
           if (!ok) break;
           ++issued;
-          if (on) tma_load_2d(qs + stg + f * UM_STG_BYTES + lane * TILE * 128, map, 0, row, sfull0 + 8 * f);
+          if (lane < nv) tma_load_2d(qs + stg + f * UM_STG_BYTES + lane * TILE * 128, map, 0, row, sfull0 + 8 * f);
         }
         if (*abort_flag && lane == 0) {  // copies into the staging ring may still be landing
           for (int jj = max(0, issued - UM_FS); jj < issued; ++jj) settle(sfull0 + 8 * (jj % UM_FS), (jj / UM_FS) & 1);
@@ -662,14 +590,13 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
         int issued = 0;
         for (int j = 0; j < nt && ok; ++j) {
           int row = 0;
-          const int t0 = key0(j) + lane * TILE;
-          const bool on = lane < UM_SLABS && t0 < nkeys && !(WIN && wk.hides(t0, TILE));  // this lane's slab is read
-          if (on) {
+          const int t0 = j * UM_KEYS + lane * TILE;
+          if (lane < UM_SLABS && t0 < nkeys) {
             const int lb = t0 / a.B;
             const int blk = tbl_in_smem ? tbl[lb] : block_at(lb);
             row = ((blk * a.L + a.layer) * a.H_kv + g) * a.B + (t0 - lb * a.B);
           }
-          const int nv = __popc(__ballot_sync(0xffffffffu, on));
+          const int nv = min(UM_SLABS, (nkeys - j * UM_KEYS + TILE - 1) / TILE);
           const int slot = j % KS;
           if (lane == 0) {
             if (j >= KS) ok = wait(empty0 + 8 * slot, ((j / KS) - 1) & 1, 100 + j);
@@ -678,7 +605,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;  // also orders the expect_tx before the copies
           if (!ok) break;
           issued += 1;
-          if (on) {
+          if (lane < nv) {
             if (kw) {  // K slab i: two 2 KB boxes, one per d chunk ([chunk][64 keys][128 B])
               const uint32_t dst = ks0 + slot * UM_KV_BYTES + lane * TILE * 128;
               tma_load_2d(dst, &tmk, 0, row, k_full + 8 * slot);
@@ -687,25 +614,22 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
               tma_load_3d(vs0 + slot * UM_KV_BYTES + lane * 2 * TILE * 128, &tmv3, 0, row, 0, v_full + 8 * slot);
             }
           }
-          if (!kw && zeroed(j)) {
-            // zero the V rows that no row sees once the tile has landed
+          if (!kw && tail && j == nt - 1) {
+            // zero the V rows past the sequence end once the tile has landed
             bool landed = true;
             if (lane == 0) landed = wait(v_full + 8 * slot, (j / KS) & 1, 200);
             landed = __shfl_sync(0xffffffffu, landed ? 1 : 0, 0) != 0;
             if (landed) {
               uint8_t* vt = base + 2 * UM_TILE_BYTES + (KS + slot) * UM_KV_BYTES;
-              auto zero_rows = [&](int r0, int r1) {
-                for (int k = lane; k < (r1 - r0) * 16; k += 32) {  // 16-byte pieces, both d chunks
-                  const int r = r0 + k / 16, c = k % 16;
-                  *reinterpret_cast<int4*>(vt + (r / TILE) * 4096 + (c / 8) * 2048 + (r % TILE) * 128 + (c % 8) * 16) =
-                      make_int4(0, 0, 0, 0);
-                }
-              };
-              if (tail && j == nt - 1) zero_rows(nkeys - key0(j), UM_KEYS);
-              if (window_edge(j)) zero_rows(hidden0(j), hidden1(j));
+              const int r0 = nkeys - j * UM_KEYS;
+              for (int k = lane; k < (UM_KEYS - r0) * 16; k += 32) {  // 16-byte pieces, both d chunks
+                const int r = r0 + k / 16, c = k % 16;
+                *reinterpret_cast<int4*>(vt + (r / TILE) * 4096 + (c / 8) * 2048 + (r % TILE) * 128 + (c % 8) * 16) =
+                    make_int4(0, 0, 0, 0);
+              }
               fence_proxy_async();
               __syncwarp();
-              if (lane == 0) mbar_arrive(vz + 8 * vz_of(j));
+              if (lane == 0) mbar_arrive(vz);
             }
           }
         }
@@ -756,7 +680,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
             progressed = true;
           }
           if (j < i && mbar_test(p_full + 8 * (2 * X + (j & 1)), (j >> 1) & 1) &&
-              mbar_test(v_full + 8 * (j % KS), (j / KS) & 1) && (KV8 || !zeroed(j) || mbar_test(vz + 8 * vz_of(j), 0))) {
+              mbar_test(v_full + 8 * (j % KS), (j / KS) & 1) && (KV8 || !tail || j < nt - 1 || mbar_test(vz, 0))) {
             tc_fence_after();
             pv(j++);
             progressed = true;
@@ -788,7 +712,6 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
       const int qi = i0 + X * QB + r / G, h = r % G;
       const bool valid = r < QB * G && qi < i1;
       const int lim = (valid && !SH) ? P + qi : pmax;  // last visible key
-      const int low = WIN ? visible_at(a.window, a.n_sink, lim).lo : 0;  // keys below it and past the sinks are hidden
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       // E4M3 pools: this warpgroup converts a staged tile of codes (K or V of key tile c) into
@@ -803,15 +726,14 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
         if (!__all_sync(0xffffffffu, ok2)) return false;
         const uint8_t* src = base + stg_off + ((is_k ? 0 : UM_FS) + f) * UM_STG_BYTES;
         uint8_t* dst = base + 2 * UM_TILE_BYTES + ((is_k ? 0 : KS) + slot) * UM_KV_BYTES;
-        const int r0 = nkeys - key0(c);  // tile rows at or past r0 are past the sequence end
-        const int h0 = WIN ? hidden0(c) : 0, h1 = WIN ? hidden1(c) : 0;  // rows h0 .. h1 - 1 no row sees
+        const int r0 = nkeys - c * UM_KEYS;  // tile rows at or past r0 are past the sequence end
 #pragma unroll
         for (int k = 0; k < UM_STG_BYTES / 16 / 128; ++k) {
           const int idx = r + 128 * k;
           const int i = idx >> 7, rr = (idx >> 3) & 15, u = idx & 7, R = TILE * i + rr;
           const uint4 w = *reinterpret_cast<const uint4*>(src + i * (TILE * 128) + rr * 128 + ((u ^ (rr & 7)) << 4));
           uint4 o0 = make_uint4(0, 0, 0, 0), o1 = make_uint4(0, 0, 0, 0);
-          if (is_k || (R < r0 && !(WIN && R >= h0 && R < h1))) {
+          if (is_k || R < r0) {
             e4m3x4_to_f16x4(w.x, o0.x, o0.y);
             e4m3x4_to_f16x4(w.y, o0.z, o0.w);
             e4m3x4_to_f16x4(w.z, o1.x, o1.y);
@@ -850,7 +772,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < NC; ++c) tmem_ld32(s_addr + 32 * c, sv[c]);
         tmem_ld_wait();
-        const int k0 = key0(j);
+        const int k0 = j * UM_KEYS;
         // mask only tiles where some row of the warp meets the causal edge or the sequence end
         if (__any_sync(0xffffffffu, k0 + UM_KEYS - 1 > lim)) {
 #pragma unroll
@@ -858,15 +780,6 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (k0 + 32 * c + e > lim) sv[c][e] = __float_as_uint(-INFINITY);
-        }
-        if constexpr (WIN) {
-          if (__any_sync(0xffffffffu, max(k0, a.n_sink) < min(k0 + UM_KEYS, low))) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (k0 + 32 * c + e < low && k0 + 32 * c + e >= a.n_sink) sv[c][e] = __float_as_uint(-INFINITY);
-          }
         }
         // row max on the raw scores (the scale is positive), 8 independent chains
         float mx8[8];
@@ -881,7 +794,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
         const float sl = a.scale_log2;
         const float m_new = fmaxf(m, mx * sl);
         if (__any_sync(0xffffffffu, m_new > m + 8.f)) {  // the reference max moves: rescale l and O so far
-          const float alpha = WIN && m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+          const float alpha = fast_exp2(m - m_new);
           if (j > 0) {
             ok = __all_sync(0xffffffffu, wait(o_done + 8 * (2 * X + ((j - 1) & 1)), ((j - 1) >> 1) & 1, 800 + j));
             if (!ok) break;
@@ -901,7 +814,7 @@ __global__ void __launch_bounds__(UM_THREADS, 1) prefill_umma_kernel(const __gri
         }
         // P = 2^(scale * s - m), 16-bit, two keys per TMEM column, written over the S just
         // read (this lane's row only: its S is in registers); 8 partial sums
-        const float neg_m = WIN && m == -INFINITY ? 0.f : -m;
+        const float neg_m = -m;
         float ls8[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) ls8[t] = 0.f;
@@ -1110,26 +1023,6 @@ int launch_prefix_share(Pool& P, const DecodeArgs& a, const void* q, const void*
   return PKV_OK;
 }
 
-namespace {
-
-template <bool WIN>
-const void* umma_kernel(int32_t dtype) {
-  if (dtype == PKV_E4M3) return reinterpret_cast<const void*>(&prefill_umma_kernel<__nv_bfloat16, true, false, WIN>);
-  if (dtype == PKV_BF16) return reinterpret_cast<const void*>(&prefill_umma_kernel<__nv_bfloat16, false, false, WIN>);
-  return reinterpret_cast<const void*>(&prefill_umma_kernel<__half, false, false, WIN>);
-}
-
-template <bool WIN>
-const void* mma_kernel(bool bf16, int d) {
-  if (d == 128)
-    return bf16 ? reinterpret_cast<const void*>(&prefill_tc_kernel<__nv_bfloat16, 128, WIN>)
-                : reinterpret_cast<const void*>(&prefill_tc_kernel<__half, 128, WIN>);
-  return bf16 ? reinterpret_cast<const void*>(&prefill_tc_kernel<__nv_bfloat16, 64, WIN>)
-              : reinterpret_cast<const void*>(&prefill_tc_kernel<__half, 64, WIN>);
-}
-
-}  // namespace
-
 int launch_prefill(Pool& P, int32_t layer, const void* q, const int32_t* q_off, int32_t n_tok, int32_t max_q,
                    const void* k_pool, const void* v_pool, const int32_t* tables, int32_t W, const int32_t* seq_lens,
                    int32_t n_seq, float scale, void* out, void* stream, const Window& win) {
@@ -1139,21 +1032,27 @@ int launch_prefill(Pool& P, int32_t layer, const void* q, const int32_t* q_off, 
   DecodeArgs a;
   if (int rc = fill_args(P, layer, q, out, tables, W, seq_lens, n_seq, scale, win, &a)) return rc;
   a.n_tok = n_tok;
-  const bool windowed = win.size > 0;
   cudaError_t e = cudaSuccess;
+  if (win.size > 0 && win_prefill_ok(g)) {
+    if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15))
+      return fail(PKV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    return launch_prefill_window(P, a, q, q_off, n_tok, max_q, k_pool, v_pool, st);
+  }
   const int64_t rows = g.num_blocks * g.L * g.H_kv * g.block_size;
-  const bool tc = (g.dtype == PKV_BF16 || g.dtype == PKV_F16) && (g.d_head == 64 || g.d_head == 128) &&
-                  G <= PF_ROWS && g.block_size % TILE == 0 && rows < (int64_t(1) << 31) && encode_fn() != nullptr;
+  const bool tc = win.size == 0 && (g.dtype == PKV_BF16 || g.dtype == PKV_F16) &&
+                  (g.d_head == 64 || g.d_head == 128) && G <= PF_ROWS && g.block_size % TILE == 0 && rows < (int64_t(1) << 31) && encode_fn() != nullptr;
   static const bool force_mma_sync = std::getenv("PKV_PREFILL_MMA_SYNC") != nullptr;
   // E4M3 pools with d_head 128: the same tcgen05 kernel on binary16 operands converted in shared memory
-  const bool tc8 = g.dtype == PKV_E4M3 && g.d_head == 128 && G <= PF_ROWS && g.block_size % TILE == 0 &&
+  const bool tc8 = win.size == 0 && g.dtype == PKV_E4M3 && g.d_head == 128 && G <= PF_ROWS && g.block_size % TILE == 0 &&
                    rows < (int64_t(1) << 31) && encode_fn() != nullptr;
   if ((tc && g.d_head == 128 && !force_mma_sync) || tc8) {
     if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15))
       return fail(PKV_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
     CUtensorMap maps[3];
     if (int rc = umma_maps(P, q, n_tok, k_pool, v_pool, tc8, maps)) return rc;
-    const void* k = windowed ? umma_kernel<true>(g.dtype) : umma_kernel<false>(g.dtype);
+    const void* k = tc8 ? reinterpret_cast<const void*>(&prefill_umma_kernel<__nv_bfloat16, true>)
+                    : g.dtype == PKV_BF16 ? reinterpret_cast<const void*>(&prefill_umma_kernel<__nv_bfloat16, false>)
+                                          : reinterpret_cast<const void*>(&prefill_umma_kernel<__half, false>);
     const int smem = um_smem(tc8);
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
@@ -1179,7 +1078,10 @@ int launch_prefill(Pool& P, int32_t layer, const void* q, const int32_t* q_off, 
     const int QB = PF_ROWS / G;
     dim3 grid((max_q + QB - 1) / QB, g.H_kv, n_seq);
     const bool bf = g.dtype == PKV_BF16;
-    const void* k = windowed ? mma_kernel<true>(bf, g.d_head) : mma_kernel<false>(bf, g.d_head);
+    const void* k = g.d_head == 128 ? (bf ? reinterpret_cast<const void*>(&prefill_tc_kernel<__nv_bfloat16, 128>)
+                                          : reinterpret_cast<const void*>(&prefill_tc_kernel<__half, 128>))
+                                    : (bf ? reinterpret_cast<const void*>(&prefill_tc_kernel<__nv_bfloat16, 64>)
+                                          : reinterpret_cast<const void*>(&prefill_tc_kernel<__half, 64>));
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
     int cap = blk_cap;

@@ -1,0 +1,792 @@
+// Chunked-prefill attention with a sliding window and sinks on the 5th-generation tensor cores.
+//
+// What it computes: query i of sequence s's chunk, at position p = len_s - C_s + i, sees the keys t <= p with
+// t > p - window or t < n_sink; out = softmax(scale q K^T) V over those (bf16, f16 and E4M3 pools, d_head 128, and 64
+// for the 16-bit pools; the block size a multiple of 16).
+//
+// Work: an item is a (sequence, KV head, pair of query blocks); its rows are two M = 128 tiles A and B of (query, head)
+// pairs (row r = query r / G, head r % G).  The keys that some query of the item sees are a list of 16-token slabs --
+// the sinks' slabs, then those from the window's start to the last query -- taken 8 slabs (128 keys) at a time, so that a
+// few sinks cost one slab, not a tile of their own.  Slabs lie in pool blocks of their own: each is one or two TMA boxes.
+//
+// What bounds it: 4 d flops a (row, key) on the tensor cores, against 128 exponentials a row and key tile on the CUDA
+// cores; the two products of a tile (A) run while the softmax of the other (B) does, so the longer of the two counts.
+// N = 128 keys a product lets its shared-memory reads (A and B operands, 8 KB a K = 16 step) keep up with the
+// multiplies, which N = 64 does not.  A window makes items short (a window of 1,024 is 9 key tiles), so what surrounds them
+// counts: the grid is persistent, and loads, products and softmax of the next item start while this one's rows are written.
+//
+// Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 issues
+// the products; 10 zeroes V rows that no row sees (0 times whatever lies there must stay 0); 11 loads Q.  E4M3 pools:
+// 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16 operands.
+// TMEM: S of A and B (128 columns each; P overwrites its first 64), O of A and B from column 256 on.
+// Order of the tensor pipe: ..., P V(A, j), Q K(A, j + 1), P V(B, j), Q K(B, j + 1), ...: one thread issues all, so a
+// product sees the earlier ones done, and the arrival of S(j + 1) says that O holds P V(j).
+//
+// Few items (a short chunk, one sequence) leave SMs idle: there a cluster of up to 8 CTAs takes one item, each a
+// range of its key tiles, and the partial (m, l, O) meet in shared memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <string>
+
+#include "pkv_attn.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+namespace {
+
+constexpr int WP_KEYS = 128, WP_SLABS = WP_KEYS / TILE;
+constexpr int WP_TBL = 384;  // entries of the table that finds an item's sequence
+
+template <bool KV8, int D>
+struct WpCfg {
+  static constexpr int THREADS = KV8 ? 512 : 384;
+  static constexpr int NCH = D / 64;                      // 64-wide chunks of d (128 bytes, the swizzle's width)
+  static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
+  static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile as an operand (16-bit)
+  static constexpr int STG_TILE = WP_KEYS * D;            // one K or V tile of E4M3 codes
+  static constexpr int KS = KV8 ? 3 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
+  static constexpr int FS = KV8 ? 4 : 0;                  // staging ring
+  static constexpr int BARS = 2 + 1 + 2 * KS + KS + 2 + 2 + 2 + 2 * 4 + 1;
+  static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
+  static constexpr int SMEM = 1024 + DATA + BARS * 8 + 16 + 64 + (WP_TBL + 1) * 4;
+  // registers: the launch's share is 65,536 / THREADS (a multiple of 8: 168 and 128)
+  static constexpr int R_SOFTMAX = KV8 ? 184 : 208, R_CONTROL = KV8 ? 64 : 56, R_CONVERT = 72;
+  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 128 * R_CONVERT : 0) <= THREADS * (KV8 ? 128 : 168),
+                "register split");
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+__device__ __forceinline__ bool wait_hint(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// One item: where its rows and keys are.
+struct Item {
+  int32_t s, g;
+  int32_t qbeg, i0, i1, nq;              // chunk's first row; its queries i0 .. i1 - 1; tiles with rows (1, 2)
+  int32_t P, nkeys;                      // position of query 0; keys up to the last query
+  int32_t sink_end, lo;                  // a key t is hidden from every row if sink_end <= t < lo
+  int32_t sink_slabs, first, nslab;      // the slab list: 0 .. sink_slabs - 1, then from `first` on
+  int32_t j0, j1;                        // this CTA's key tiles
+  __device__ __forceinline__ int32_t slab(int32_t u) const { return u < sink_slabs ? u : first + u - sink_slabs; }
+  __device__ __forceinline__ int32_t slabs_of(int32_t j) const { return min(WP_SLABS, nslab - j * WP_SLABS); }
+  __device__ __forceinline__ bool hidden(int32_t t) const { return t >= nkeys || (t >= sink_end && t < lo); }
+  __device__ __forceinline__ bool ragged(int32_t u) const {  // slab u holds a key hidden from every row
+    return hidden(slab(u) * TILE) || hidden(slab(u) * TILE + TILE - 1) ||
+           (sink_end < lo && slab(u) * TILE < lo && slab(u) * TILE + TILE > sink_end);
+  }
+  // tile j holds such a slab: only the last with sinks, the first after them and the last can
+  __device__ __forceinline__ bool zeroes(int32_t j) const {
+    const int32_t a = j * WP_SLABS, b = a + slabs_of(j);
+    auto at = [&](int32_t u) { return u >= a && u < b && ragged(u); };
+    return at(sink_slabs - 1) || at(sink_slabs) || at(nslab - 1);
+  }
+};
+
+template <typename T, bool KV8, int D>
+__global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
+    prefill_win_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, const DecodeArgs a, const int32_t* __restrict__ q_off,
+                       int32_t max_q, int32_t csize, int64_t most_items) {
+  using C = WpCfg<KV8, D>;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // operand type of the products
+  using TP = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int KS = C::KS, FS = C::FS;
+  extern __shared__ uint8_t smem_raw[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.G, QB = 128 / G;  // queries a tile
+  const int rank = csize > 1 ? blockIdx.x % csize : 0;
+
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t qs = smem_u32(base), ring = qs + 2 * C::Q_TILE;
+  uint8_t* ring_p = base + 2 * C::Q_TILE;
+  uint8_t* stg_p = ring_p + KS * C::KV_TILE;
+  uint8_t* bar_p = base + C::DATA;
+  const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
+  const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
+  const uint32_t s_full = land + 8 * KS, p_full = s_full + 16, o_full = p_full + 16;  // per tile A, B
+  const uint32_t sf_full = o_full + 16, sf_empty = sf_full + 32, drain = sf_empty + 32;  // staging ring
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar_p + C::BARS * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  int32_t* wsum = reinterpret_cast<int32_t*>(tslot + 4);
+  int32_t* pre = wsum + 16;  // [groups + 1]: query-block pairs of the sequences before a group of them
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_ready, 128);
+    mbar_init(q_empty, 1);
+    for (int k = 0; k < KS; ++k) {
+      mbar_init(full + 8 * k, KV8 ? 128 : 1);
+      mbar_init(empty + 8 * k, 1);
+      mbar_init(land + 8 * k, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full + 8 * x, 1);
+      mbar_init(p_full + 8 * x, 128);
+      mbar_init(o_full + 8 * x, 1);
+    }
+    for (int k = 0; k < FS; ++k) {
+      mbar_init(sf_full + 8 * k, 1);
+      mbar_init(sf_empty + 8 * k, 128);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) tmem_alloc(smem_u32(tslot), 512);
+
+  // ---- the items, counted ahead so that ragged chunks leave no holes: a thread counts the query-block pairs of
+  // `per` sequences (one, up to WP_TBL of them), and the table holds the sums before each such group
+  const int most = (max_q + 2 * QB - 1) / (2 * QB);  // query-block pairs of a chunk at most
+  const int per = (a.n_seq + WP_TBL - 1) / WP_TBL, groups = (a.n_seq + per - 1) / per;
+  auto pairs_of = [&](int s, bool record) -> int {
+    const int q0 = q_off[s], c = q_off[s + 1] - q0;
+    if (q0 < 0 || c < 0 || c > a.n_tok - q0) {
+      if (record) record_error(a.err, DERR_PREFILL_CHUNK, s);
+      return 0;
+    }
+    return min(most, (c + 2 * QB - 1) / (2 * QB));
+  };
+  {
+    int n = 0;
+    if (tid < groups)
+      for (int s = tid * per; s < min(a.n_seq, (tid + 1) * per); ++s) n += pairs_of(s, blockIdx.x == 0);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) incl += wsum[k];
+    if (tid < groups) pre[tid + 1] = incl;
+    if (tid == 0) pre[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  const int64_t n_items = min(static_cast<int64_t>(pre[groups]) * a.H_kv, most_items);
+  const int64_t step = csize > 1 ? n_items : gridDim.x;  // a cluster takes one item
+  const int64_t begin = csize > 1 ? blockIdx.x / csize : blockIdx.x;
+
+  // item idx; false for one without work.  Every role calls it for the same items; `record` reports bad values.
+  auto get = [&](int64_t idx, Item& w, bool record) __attribute__((always_inline)) -> bool {
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(pre[mid]) * a.H_kv <= idx) lo = mid; else hi = mid - 1;
+    }
+    int64_t r = idx - static_cast<int64_t>(pre[lo]) * a.H_kv;
+    w.s = lo * per;
+    int nb = pairs_of(w.s, false);
+    while (r >= static_cast<int64_t>(nb) * a.H_kv && w.s + 1 < a.n_seq) {
+      r -= static_cast<int64_t>(nb) * a.H_kv;
+      nb = pairs_of(++w.s, false);
+    }
+    if (nb == 0 || r < 0 || r >= static_cast<int64_t>(nb) * a.H_kv) return false;
+    w.g = static_cast<int>(r) / nb;
+    const int qb = static_cast<int>(r) - w.g * nb;
+    w.qbeg = q_off[w.s];
+    const int Cs = q_off[w.s + 1] - w.qbeg, len = a.seq_lens[w.s];
+    record = record && qb == 0 && w.g == 0;
+    if (record && Cs > max_q) record_error(a.err, DERR_PREFILL_CHUNK, w.s);
+    w.i0 = qb * 2 * QB;
+    if (w.i0 >= Cs) return false;
+    if (len < Cs || len > static_cast<int64_t>(a.W) * a.B) {
+      if (record) record_error(a.err, DERR_DECODE_LEN, w.s);
+      return false;
+    }
+    w.nq = w.i0 + QB < Cs ? 2 : 1;
+    w.i1 = min(Cs, w.i0 + w.nq * QB);
+    w.P = len - Cs;
+    w.nkeys = w.P + w.i1;
+    const Visible v = visible_at(a.window, a.n_sink, w.P + w.i0);
+    w.sink_end = v.ns;
+    w.lo = v.lo;
+    w.sink_slabs = (v.ns + TILE - 1) / TILE;
+    w.first = max(w.sink_slabs, v.lo / TILE);
+    w.nslab = w.sink_slabs + (w.nkeys + TILE - 1) / TILE - w.first;
+    const int nt = (w.nslab + WP_SLABS - 1) / WP_SLABS;
+    w.j0 = static_cast<int>(static_cast<int64_t>(nt) * rank / csize);
+    w.j1 = static_cast<int>(static_cast<int64_t>(nt) * (rank + 1) / csize);
+    return true;
+  };
+
+  // bounded wait that also gives up once another role has given up
+  auto wait = [&](uint32_t bar, uint32_t parity, int where) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+      if (wait_hint(bar, parity)) return true;
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > kWaitNs) {
+        *abort_flag = 1;
+        record_error(a.err, DERR_DECODE_TIMEOUT, where);
+        return false;
+      }
+    }
+  };
+  // after an abort: bounded wait for copies or products already started
+  auto settle = [&](uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity) && global_ns() - t0 < kWaitNs) {
+    }
+  };
+  auto warp_ok = [&](bool ok) { return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0; };
+
+  Item w;
+  bool ok = true;
+  if (warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_CONTROL));
+    if (warp == 8) {
+      // ------------------------------------------------------------ K and V tiles, in turn, into the ring
+      // Lane i holds the pool row of slab 32 k + i of the list (the next 32 are looked up ahead); the 8 lanes of tile
+      // j copy its slabs.  16-bit pools: a K slab as one box per 64-wide chunk ([chunk][128 keys][128 B]), a V slab
+      // as one box of all chunks ([slab][chunk][16 keys][128 B]); E4M3 pools: 2 KB of codes into the staging ring.
+      constexpr int RS = KV8 ? FS : KS;
+      const uint32_t r_full = KV8 ? sf_full : full, r_empty = KV8 ? sf_empty : empty;
+      const uint32_t r_data = KV8 ? smem_u32(stg_p) : ring;
+      uint32_t c = 0;  // tiles loaded so far
+      uint32_t on_land = 0;  // of the last RS tiles, those whose bytes arrive at `land` (bit c % RS)
+      uint32_t land_par = 0;  // bit k: parity of the uses of `land` slot k
+      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+        if (!get(idx, w, false)) continue;
+        auto row_of = [&](int u) -> int {
+          if (u >= w.nslab) return 0;
+          const int t0 = w.slab(u) * TILE, lb = t0 / a.B;
+          int blk = a.tables[static_cast<int64_t>(w.s) * a.W + lb];
+          if (blk < 0 || blk >= a.num_blocks) {
+            record_error(a.err, DERR_DECODE_BLOCK, blk);
+            blk = 0;
+          }
+          return ((blk * a.L + a.layer) * a.H_kv + w.g) * a.B + (t0 - lb * a.B);
+        };
+        constexpr int TPG = 32 / WP_SLABS;  // tiles a group of 32 slabs
+        int row = row_of(w.j0 * WP_SLABS + lane);
+        int next = w.j0 + TPG < w.j1 ? row_of((w.j0 + TPG) * WP_SLABS + lane) : 0;
+        for (int j = w.j0; j < w.j1 && ok; ++j) {
+          const int q = (j - w.j0) % TPG;
+          if (q == 0 && j > w.j0) {
+            row = next;
+            if (j + TPG < w.j1) next = row_of((j + TPG) * WP_SLABS + lane);
+          }
+          const int ns = w.slabs_of(j), i = lane - q * WP_SLABS;  // this lane's slab of the tile
+          const bool mine = i >= 0 && i < ns;
+          for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
+            const uint32_t slot = c % RS;
+            const bool zero = !KV8 && kv == 1 && w.zeroes(j);
+            const uint32_t bar = zero ? land + 8 * slot : r_full + 8 * slot;
+            if (lane == 0) {
+              if (c >= RS) ok = wait(r_empty + 8 * slot, ((c / RS) - 1) & 1, 100);
+              if (ok) mbar_arrive_expect_tx(bar, ns * TILE * D * (KV8 ? 1 : 2));
+            }
+            ok = warp_ok(ok);  // also orders the expect_tx before the copies
+            if (!ok) break;
+            on_land = (on_land & ~(1u << slot)) | (zero ? 1u << slot : 0u);
+            if (zero) land_par ^= 1u << slot;
+            const uint32_t dst = r_data + slot * (KV8 ? C::STG_TILE : C::KV_TILE);
+            if (mine) {
+              if constexpr (KV8) {
+                tma_load_2d(dst + i * TILE * 128, kv ? &tmv : &tmk, 0, row, bar);
+              } else if (kv == 0) {
+#pragma unroll
+                for (int h = 0; h < C::NCH; ++h)
+                  tma_load_2d(dst + h * (WP_KEYS * 128) + i * TILE * 128, &tmk, 64 * h, row, bar);
+              } else if constexpr (D == 128) {
+                tma_load_3d(dst + i * 2 * TILE * 128, &tmv, 0, row, 0, bar);
+              } else {
+                tma_load_2d(dst + i * TILE * 128, &tmv, 0, row, bar);
+              }
+            }
+          }
+        }
+      }
+      if (*abort_flag && lane == 0)  // copies may still be landing in the last ring's slots
+        for (uint32_t k = c > RS ? c - RS : 0; k < c; ++k) {
+          const uint32_t slot = k % RS;
+          if (!KV8 && (on_land >> slot & 1)) settle(land + 8 * slot, ~(land_par >> slot) & 1);
+          else settle(r_full + 8 * slot, (k / RS) & 1);
+        }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ the products, one thread
+      if (lane == 0) {
+        const uint32_t idesc_o = umma_idesc_f16(BF16, 128, D, true);
+        uint32_t c = 0, items = 0, np = 0;  // ring position; items; bit x: parity of the P tiles taken of A, B
+        auto qk = [&](int x, uint32_t slot, int ns) {
+          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, ns * TILE, false);
+          const uint32_t kb = ring + slot * C::KV_TILE, qx = qs + x * C::Q_TILE;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t kin = (k & 3) * 32;  // 16 elements along the swizzled 128-byte row
+            umma_ss(tmem + 128 * x, umma_desc_sw128(qx + (k >> 2) * 16384 + kin, 16, 1024),
+                    umma_desc_sw128(kb + (k >> 2) * (WP_KEYS * 128) + kin, 16, 1024), idesc_s, k > 0);
+          }
+          umma_commit(s_full + 8 * x);
+        };
+        auto pv = [&](int x, uint32_t slot, int ns, bool acc) {
+          const uint32_t vb = ring + slot * C::KV_TILE;
+          for (int k = 0; k < ns; ++k)
+            umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k,
+                    umma_desc_sw128(vb + k * (C::NCH * TILE * 128), TILE * 128, 1024), idesc_o, acc || k > 0 ? 1u : 0u);
+        };
+        for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+          if (!get(idx, w, false)) continue;
+          if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
+          ok = wait(KV8 ? q_ready : q_full, items & 1, 200);
+          if (ok) ok = wait(full + 8 * (c % KS), (c / KS) & 1, 210);
+          if (!ok) break;
+          tc_fence_after();
+          for (int x = 0; x < w.nq; ++x) qk(x, c % KS, w.slabs_of(w.j0));
+          umma_commit(empty + 8 * (c % KS));
+          ++c;
+          if (w.j1 - w.j0 == 1) umma_commit(q_empty);
+          for (int j = w.j0; j < w.j1 && ok; ++j) {
+            const uint32_t vc = c, kc = c + 1;  // V(j), K(j + 1)
+            const bool more = j + 1 < w.j1;
+            for (int x = 0; x < w.nq && ok; ++x) {
+              ok = wait(p_full + 8 * x, np >> x & 1, 220);
+              if (ok && x == 0) ok = wait(full + 8 * (vc % KS), (vc / KS) & 1, 230);
+              if (!ok) break;
+              np ^= 1u << x;
+              tc_fence_after();
+              pv(x, vc % KS, w.slabs_of(j), j > w.j0);
+              if (!more) umma_commit(o_full + 8 * x);
+              if (x == w.nq - 1) umma_commit(empty + 8 * (vc % KS));
+              if (more) {
+                if (x == 0) ok = wait(full + 8 * (kc % KS), (kc / KS) & 1, 240);
+                if (!ok) break;
+                tc_fence_after();
+                qk(x, kc % KS, w.slabs_of(j + 1));
+                if (x == w.nq - 1) {
+                  umma_commit(empty + 8 * (kc % KS));
+                  if (j + 2 == w.j1) umma_commit(q_empty);  // the item's last use of Q
+                }
+              }
+            }
+            c += more ? 2 : 1;
+          }
+          ++items;
+        }
+        if (*abort_flag) {
+          umma_commit(drain);
+          settle(drain, 0);
+        }
+      }
+    } else if (warp == 10) {
+      // ------------------------------------------------------------ V rows hidden from every row of the item
+      if (!KV8) {
+        uint32_t c = 0, uses = 0;  // ring position; bit k: parity of `land` uses of slot k
+        for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+          if (!get(idx, w, false)) continue;
+          for (int j = w.j0; j < w.j1 && ok; ++j, c += 2) {
+            if (!w.zeroes(j)) continue;
+            const uint32_t slot = (c + 1) % KS;
+            if (lane == 0) ok = wait(land + 8 * slot, uses >> slot & 1, 300);
+            ok = warp_ok(ok);
+            if (!ok) break;
+            uses ^= 1u << slot;
+            uint8_t* vt = ring_p + slot * C::KV_TILE;
+            for (int i = 0; i < w.slabs_of(j); ++i) {
+              const int u = j * WP_SLABS + i;
+              if (!w.ragged(u)) continue;
+              const int t0 = w.slab(u) * TILE;
+              for (int k = lane; k < TILE * 8 * C::NCH; k += 32) {  // 16-byte pieces of the slab
+                const int r = k / (8 * C::NCH), p = k % (8 * C::NCH);
+                if (w.hidden(t0 + r))
+                  *reinterpret_cast<int4*>(vt + i * (C::NCH * TILE * 128) + p / 8 * (TILE * 128) + r * 128 + p % 8 * 16) =
+                      make_int4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * slot);
+          }
+        }
+      }
+    } else if (lane == 0) {
+      // ------------------------------------------------------------ Q
+      uint32_t items = 0;
+      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+        if (!get(idx, w, false) || w.j0 == w.j1) continue;
+        if (items > 0) ok = wait(q_empty, (items - 1) & 1, 400);
+        if (!ok) break;
+        fence_proxy_async();
+        mbar_arrive_expect_tx(q_full, w.nq * G * QB * D * 2);  // G * QB rows a tile (126 for G = 3)
+        for (int x = 0; x < w.nq; ++x)
+          for (int h = 0; h < C::NCH; ++h)
+            tma_load_3d(qs + x * C::Q_TILE + h * 16384, &tmq, 64 * h, w.g * G, w.qbeg + w.i0 + x * QB, q_full);
+        ++items;
+      }
+      if (*abort_flag && items > 0) settle(q_full, (items - 1) & 1);
+    }
+  } else if (warp >= 12) {
+    // -------------------------------------------------------------- E4M3: q and the staged codes to binary16
+    if constexpr (KV8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_CONVERT));
+      const int r = tid & 127;
+      uint32_t c = 0, items = 0;
+      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+        if (!get(idx, w, false) || w.j0 == w.j1) continue;
+        ok = __all_sync(0xffffffffu, wait(q_full, items & 1, 500));
+        if (!ok) break;
+        for (int k = r; k < w.nq * C::Q_TILE / 16; k += 128) {
+          uint4 v = reinterpret_cast<uint4*>(base)[k];
+          uint32_t* p = &v.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(p[e] << 16), __uint_as_float(p[e] & 0xffff0000u));
+            p[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          reinterpret_cast<uint4*>(base)[k] = v;
+        }
+        fence_proxy_async();
+        mbar_arrive(q_ready);
+        ++items;
+        for (int j = w.j0; j < w.j1 && ok; ++j)
+          for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
+            const uint32_t f = c % 4, slot = c % KS;
+            bool here = wait(sf_full + 8 * f, (c / 4) & 1, 510);
+            if (here && c >= KS) here = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 520);
+            ok = __all_sync(0xffffffffu, here);
+            if (!ok) break;
+            const uint8_t* src = stg_p + f * C::STG_TILE;
+            uint8_t* dst = ring_p + slot * C::KV_TILE;
+            const int ns = w.slabs_of(j);
+            const bool zero = kv == 1 && w.zeroes(j);
+            // staging row rr of slab i holds d = 16 u .. 16 u + 15 in 16-byte unit u ^ (rr & 7); the operand rows hold
+            // d in two 64-wide chunks of eight units, unit t at t ^ (row & 7).  Thread r: row r / 8, unit r % 8 of slab i
+            const int rr = r >> 3, u = r & 7, cc = u >> 2, t = (u & 3) * 2, sw = rr & 7;
+#pragma unroll 4
+            for (int i = 0; i < ns; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src + i * (TILE * 128) + rr * 128 + ((u ^ sw) << 4));
+              uint4 o0, o1;
+              auto cvt = [](uint32_t x, uint32_t& lo, uint32_t& hi) {
+                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                    : "=r"(lo), "=r"(hi)
+                    : "r"(x));
+              };
+              cvt(v.x, o0.x, o0.y);
+              cvt(v.y, o0.z, o0.w);
+              cvt(v.z, o1.x, o1.y);
+              cvt(v.w, o1.z, o1.w);
+              if (zero && w.hidden(w.slab(j * WP_SLABS + i) * TILE + rr)) o0 = o1 = make_uint4(0, 0, 0, 0);
+              uint8_t* p = kv == 0 ? dst + cc * (WP_KEYS * 128) + (i * TILE + rr) * 128
+                                   : dst + i * 4096 + cc * 2048 + rr * 128;
+              *reinterpret_cast<uint4*>(p + ((t ^ sw) << 4)) = o0;
+              *reinterpret_cast<uint4*>(p + (((t + 1) ^ sw) << 4)) = o1;
+            }
+            fence_proxy_async();
+            mbar_arrive(full + 8 * slot);
+            mbar_arrive(sf_empty + 8 * f);
+          }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax and epilogue of tile X
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::R_SOFTMAX));
+    const int X = warp >> 2, r = tid & 127;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
+    const float sl = a.scale_log2;
+    uint32_t ns_ = 0, no = 0;  // S tiles and outputs taken
+    for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+      if (!get(idx, w, X == 0 && tid == 0 && rank == 0)) continue;
+      if (X >= w.nq) continue;
+      const int qi = w.i0 + X * QB + r / G, h = r % G;
+      const bool valid = r < QB * G && qi < w.i1;
+      const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
+      const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
+      float m = -INFINITY, l = 0.f;
+      for (int j = w.j0; j < w.j1 && ok; ++j) {
+        ok = __all_sync(0xffffffffu, wait(s_full + 8 * X, ns_ & 1, 600));
+        if (!ok) break;
+        ++ns_;
+        tc_fence_after();
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, sv[c]);
+        tmem_ld_wait();
+        // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
+        const int u0 = j * WP_SLABS, n = w.slabs_of(j);
+        const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
+        const bool edge = n < WP_SLABS || t_last > lim || t_first < low;
+        if (__any_sync(0xffffffffu, edge)) {
+#pragma unroll
+          for (int i = 0; i < WP_SLABS; ++i) {
+            // elements of slab i: e > hi is past the row's last key; sk <= e < lo_e between its sinks and its window
+            const int t0 = w.slab(u0 + i) * TILE;
+            const int hi = i < n ? lim - t0 : -1, lo_e = low - t0, sk = a.n_sink > t0 ? a.n_sink - t0 : 0;
+#pragma unroll
+            for (int e = 0; e < TILE; ++e)
+              if (e > hi || (e < lo_e && e >= sk)) sv[i >> 1][(i & 1) * TILE + e] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mx8[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mx8[t] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(sv[c][e]));
+        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        const float m_new = fmaxf(m, mx * sl);
+        // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
+        // l and O so far are rescaled; S(j) is here, so O holds P V(j - 1)
+        if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
+          const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+          if (j > w.j0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(o_addr + 32 * c, o);
+            }
+          }
+          l *= alpha;
+          m = m_new;
+        }
+        // P = 2^(scale s - m), 16-bit, two keys a column, over the S just read; a row that has seen no key yet
+        // keeps m = -inf, and 0 stands in for it
+        const float neg_m = m == -INFINITY ? 0.f : -m;
+        float ls8[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) ls8[t] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = fast_exp2(fmaf(__uint_as_float(sv[c][2 * e]), sl, neg_m));
+            const float p1 = fast_exp2(fmaf(__uint_as_float(sv[c][2 * e + 1]), sl, neg_m));
+            ls8[e & 7] += p0 + p1;
+            pw[e] = pack2<TP>(p0, p1);
+          }
+          tmem_st16(s_addr + 16 * c, pw);
+        }
+        l += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full + 8 * X);
+      }
+      if (!ok) break;
+      if (w.j0 < w.j1) {
+        ok = __all_sync(0xffffffffu, wait(o_full + 8 * X, no & 1, 700));
+        // a cluster's partial goes over the operands: not before the products of the other tile are done, too
+        if (ok && csize > 1 && X == 0 && w.nq == 2) ok = __all_sync(0xffffffffu, wait(o_full + 8, 0, 710));
+        if (!ok) break;
+        ++no;
+        tc_fence_after();
+      }
+      if (csize == 1) {
+        const float inv = a.v_mul / l;  // v_scale of an E4M3 pool, else 1
+        T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(w.qbeg + qi) * a.H_q + w.g * G + h) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + 32 * c, o);
+          tmem_ld_wait();
+          if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              dst[v] = make_uint4(pack2<T>(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                                  pack2<T>(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                                  pack2<T>(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                                  pack2<T>(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+          }
+        }
+        tc_fence_before();
+      } else {
+        // this CTA's partial of the row, over the operand room (its products are done, its loads were all used):
+        // (m, l) of the 256 rows, then O; 16-byte pieces rotated by the row so that neighbours share no bank
+        if (w.j0 < w.j1) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * c, o);
+            tmem_ld_wait();
+            if (valid) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                *reinterpret_cast<uint4*>(base + 2048 + (X * 128 + r) * (D * 4) + ((8 * c + v + r) % (D / 4)) * 16) =
+                    make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            }
+          }
+          tc_fence_before();
+        }
+        *reinterpret_cast<float2*>(base + (X * 128 + r) * 8) = make_float2(m, l);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (csize > 1) {
+    // every thread of the cluster; an item is the same for all its CTAs, and so is its absence
+    Item it;
+    const bool has = begin < n_items && get(begin, it, false);
+    cluster_barrier();
+    if (has && !*abort_flag) {
+      constexpr int PC = D / 4;  // 16-byte pieces of a row's O
+      const int rows = (it.i1 - it.i0) * G;  // rows of A (QB G of them), then of B
+      for (int k = rank * blockDim.x + tid; k < rows * PC; k += csize * blockDim.x) {
+        const int row = k / PC, pc = k - row * PC;
+        const int x = row / (QB * G), r = row - x * QB * G, at = x * 128 + r;
+        float m = -INFINITY;
+        for (int p = 0; p < csize; ++p) {
+          float pm;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pm) : "r"(cluster_peer(qs + at * 8, p)) : "memory");
+          m = fmaxf(m, pm);
+        }
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < csize; ++p) {
+          float pm, pl;
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(pm), "=f"(pl)
+                       : "r"(cluster_peer(qs + at * 8, p))
+                       : "memory");
+          if (pm == -INFINITY) continue;  // no key of the row in that CTA's range: its O holds nothing
+          float4 v;
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "r"(cluster_peer(qs + 2048 + at * (D * 4) + ((pc + r) % PC) * 16, p))
+                       : "memory");
+          const float e = fast_exp2(pm - m);
+          l += pl * e;
+          o.x += v.x * e;
+          o.y += v.y * e;
+          o.z += v.z * e;
+          o.w += v.w * e;
+        }
+        const float inv = a.v_mul / l;
+        T* out = static_cast<T*>(a.out) +
+                 (static_cast<int64_t>(it.qbeg + it.i0 + x * QB + r / G) * a.H_q + it.g * G + r % G) * D + 4 * pc;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+      }
+    }
+    cluster_barrier();  // peers may still read this CTA's partials
+  }
+}
+
+int encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* p, const cuuint64_t* dims,
+           const cuuint64_t* strides, const cuuint32_t* box, const char* what) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = encode_fn()(map, type, rank, const_cast<void*>(p), dims, strides, box, ones,
+                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(PKV_ERR_CUDA, std::string("cuTensorMapEncodeTiled (") + what + ") failed: " + std::to_string(r));
+  return PKV_OK;
+}
+
+template <typename T, bool KV8, int D>
+int launch_t(Pool& P, DecodeArgs& a, CUtensorMap* maps, const int32_t* q_off, int32_t max_q, int32_t n_tok,
+             cudaStream_t st) {
+  using C = WpCfg<KV8, D>;
+  max_q = std::min(max_q, n_tok);  // no chunk is longer than that
+  const void* k = reinterpret_cast<const void*>(&prefill_win_kernel<T, KV8, D>);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
+  // items at most: by rows (each sequence adds a ragged pair of blocks) and by the longest chunk
+  const int64_t two = 2 * (128 / a.G), most = (static_cast<int64_t>(max_q) + two - 1) / two;
+  int64_t items =
+      std::min(most * a.n_seq, static_cast<int64_t>(n_tok) / two + a.n_seq) * P.geo.H_kv;
+  // key tiles of an item at most: the table's, or those of the sinks, the window and the item's queries
+  const int64_t keys = std::min(static_cast<int64_t>(a.W) * a.B,
+                                static_cast<int64_t>(a.n_sink) + a.window + std::min<int64_t>(max_q, two) + 2 * TILE);
+  int32_t csize = 1;
+  while (csize < 8 && items * csize * 2 <= sms && keys >= 2 * csize * WP_KEYS) csize *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(csize > 1 ? items * csize : std::min<int64_t>(items, sms)));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = csize > 1 ? 1 : 0;
+  void* args[] = {&maps[0], &maps[1], &maps[2], &a, const_cast<int32_t**>(&q_off), &max_q, &csize, &items};
+  e = cudaLaunchKernelExC(&cfg, k, args);
+  if (e != cudaSuccess) return fail(PKV_ERR_CUDA, std::string("windowed prefill launch: ") + cudaGetErrorString(e));
+  count_launch();
+  return PKV_OK;
+}
+
+}  // namespace
+
+// The geometries that the kernel takes.
+bool win_prefill_ok(const pkv_geometry& g) {
+  const bool dt = ((g.dtype == PKV_BF16 || g.dtype == PKV_F16) && (g.d_head == 64 || g.d_head == 128)) ||
+                  (g.dtype == PKV_E4M3 && g.d_head == 128);
+  return dt && g.H_q / g.H_kv <= 128 && g.block_size % TILE == 0 &&
+         g.num_blocks * g.L * g.H_kv * g.block_size < (int64_t(1) << 31) && encode_fn() != nullptr;
+}
+
+int launch_prefill_window(Pool& P, DecodeArgs& a, const void* q, const int32_t* q_off, int32_t n_tok, int32_t max_q,
+                          const void* k_pool, const void* v_pool, cudaStream_t st) {
+  const auto& g = P.geo;
+  const cuuint64_t d = static_cast<cuuint64_t>(g.d_head);
+  const cuuint64_t rows = static_cast<cuuint64_t>(g.num_blocks) * g.L * g.H_kv * g.block_size;
+  const CUtensorMapDataType act =
+      g.dtype == PKV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;  // q: bf16 for E4M3
+  CUtensorMap maps[3];
+  if (int rc = get_tensor_maps(P, k_pool, v_pool, &maps[1], &maps[2])) return rc;
+  {  // q: a {64, G, 128 / G} box lands as (query, head) rows of 128 bytes
+    const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(g.H_q), static_cast<cuuint64_t>(n_tok)};
+    const cuuint64_t strides[2] = {d * 2, d * 2 * static_cast<cuuint64_t>(g.H_q)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(128 / a.G)};
+    if (int rc = encode(&maps[0], act, 3, q, dims, strides, box, "q")) return rc;
+  }
+  if (g.dtype != PKV_E4M3 && g.d_head == 128) {  // V: a {64, 16, 2} box is a slab, chunk after chunk
+    const cuuint64_t dims[3] = {64, rows, 2}, strides[2] = {256, 128};
+    const cuuint32_t box[3] = {64, TILE, 2};
+    if (int rc = encode(&maps[2], act, 3, v_pool, dims, strides, box, "v slabs")) return rc;
+  }
+  if (g.dtype == PKV_E4M3) return launch_t<__nv_bfloat16, true, 128>(P, a, maps, q_off, max_q, n_tok, st);
+  const bool bf = g.dtype == PKV_BF16;
+  if (g.d_head == 128)
+    return bf ? launch_t<__nv_bfloat16, false, 128>(P, a, maps, q_off, max_q, n_tok, st)
+              : launch_t<__half, false, 128>(P, a, maps, q_off, max_q, n_tok, st);
+  return bf ? launch_t<__nv_bfloat16, false, 64>(P, a, maps, q_off, max_q, n_tok, st)
+            : launch_t<__half, false, 64>(P, a, maps, q_off, max_q, n_tok, st);
+}
+
+}  // namespace pkv
