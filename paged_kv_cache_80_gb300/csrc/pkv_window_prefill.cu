@@ -73,6 +73,19 @@ __device__ __forceinline__ bool wait_hint(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// true in one lane of the (converged) warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
+// the lowest n of 16 bits
+__device__ __forceinline__ uint32_t below(int n) {
+  const int k = max(0, min(TILE, n));
+  return (1u << k) - 1u;
+}
+
 __device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -111,6 +124,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     prefill_win_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const DecodeArgs a, const int32_t* __restrict__ q_off,
                        int32_t max_q, int32_t csize, int64_t most_items) {
+  static_assert(WP_KEYS * 128 == 16384, "Q and K chunks are alike");
   using C = WpCfg<KV8, D>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // operand type of the products
   using TP = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -333,58 +347,72 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           else settle(r_full + 8 * slot, (k / RS) & 1);
         }
     } else if (warp == 9) {
-      // ------------------------------------------------------------ the products, one thread
-      if (lane == 0) {
+      // ------------------------------------------------------------ the products
+      // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
+      // divergent thread on its own needs some 140 cycles a product to bring its operands into uniform registers.
+      {
+        auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
+          return __all_sync(0xffffffffu, wait(bar, parity, where)) != 0;
+        };
         const uint32_t idesc_o = umma_idesc_f16(BF16, 128, D, true);
         uint32_t c = 0, items = 0, np = 0;  // ring position; items; bit x: parity of the P tiles taken of A, B
+        // operand descriptors: the first, and a step of the address field (16-byte units) from there on
+        const uint64_t q_desc = umma_desc_sw128(qs, 16, 1024), k_desc = umma_desc_sw128(ring, 16, 1024);
+        const uint64_t v_desc = umma_desc_sw128(ring, TILE * 128, 1024);
         auto qk = [&](int x, uint32_t slot, int ns) {
           const uint32_t idesc_s = umma_idesc_f16(BF16, 128, ns * TILE, false);
-          const uint32_t kb = ring + slot * C::KV_TILE, qx = qs + x * C::Q_TILE;
+          const uint64_t qd = q_desc + x * (C::Q_TILE / 16), kd = k_desc + slot * (C::KV_TILE / 16);
+          if (!elect_one()) return;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t kin = (k & 3) * 32;  // 16 elements along the swizzled 128-byte row
-            umma_ss(tmem + 128 * x, umma_desc_sw128(qx + (k >> 2) * 16384 + kin, 16, 1024),
-                    umma_desc_sw128(kb + (k >> 2) * (WP_KEYS * 128) + kin, 16, 1024), idesc_s, k > 0);
+            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) / 16;  // chunk; 16 elements along its 128-byte row
+            umma_ss(tmem + 128 * x, qd + off, kd + off, idesc_s, k > 0);
           }
           umma_commit(s_full + 8 * x);
         };
         auto pv = [&](int x, uint32_t slot, int ns, bool acc) {
-          const uint32_t vb = ring + slot * C::KV_TILE;
-          for (int k = 0; k < ns; ++k)
-            umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k,
-                    umma_desc_sw128(vb + k * (C::NCH * TILE * 128), TILE * 128, 1024), idesc_o, acc || k > 0 ? 1u : 0u);
+          const uint64_t vd = v_desc + slot * (C::KV_TILE / 16);
+          if (!elect_one()) return;
+#pragma unroll
+          for (int k = 0; k < WP_SLABS; ++k)
+            if (k < ns)
+              umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o,
+                      acc || k > 0 ? 1u : 0u);
+        };
+        auto commit = [&](uint32_t bar) {
+          if (elect_one()) umma_commit(bar);
         };
         for (int64_t idx = begin; idx < n_items && ok; idx += step) {
           if (!get(idx, w, false)) continue;
           if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
-          ok = wait(KV8 ? q_ready : q_full, items & 1, 200);
-          if (ok) ok = wait(full + 8 * (c % KS), (c / KS) & 1, 210);
+          ok = wait_all(KV8 ? q_ready : q_full, items & 1, 200);
+          if (ok) ok = wait_all(full + 8 * (c % KS), (c / KS) & 1, 210);
           if (!ok) break;
           tc_fence_after();
           for (int x = 0; x < w.nq; ++x) qk(x, c % KS, w.slabs_of(w.j0));
-          umma_commit(empty + 8 * (c % KS));
+          commit(empty + 8 * (c % KS));
           ++c;
-          if (w.j1 - w.j0 == 1) umma_commit(q_empty);
+          if (w.j1 - w.j0 == 1) commit(q_empty);
           for (int j = w.j0; j < w.j1 && ok; ++j) {
             const uint32_t vc = c, kc = c + 1;  // V(j), K(j + 1)
             const bool more = j + 1 < w.j1;
             for (int x = 0; x < w.nq && ok; ++x) {
-              ok = wait(p_full + 8 * x, np >> x & 1, 220);
-              if (ok && x == 0) ok = wait(full + 8 * (vc % KS), (vc / KS) & 1, 230);
+              ok = wait_all(p_full + 8 * x, np >> x & 1, 220);
+              if (ok && x == 0) ok = wait_all(full + 8 * (vc % KS), (vc / KS) & 1, 230);
               if (!ok) break;
               np ^= 1u << x;
               tc_fence_after();
               pv(x, vc % KS, w.slabs_of(j), j > w.j0);
-              if (!more) umma_commit(o_full + 8 * x);
-              if (x == w.nq - 1) umma_commit(empty + 8 * (vc % KS));
+              if (!more) commit(o_full + 8 * x);
+              if (x == w.nq - 1) commit(empty + 8 * (vc % KS));
               if (more) {
-                if (x == 0) ok = wait(full + 8 * (kc % KS), (kc / KS) & 1, 240);
+                if (x == 0) ok = wait_all(full + 8 * (kc % KS), (kc / KS) & 1, 240);
                 if (!ok) break;
                 tc_fence_after();
                 qk(x, kc % KS, w.slabs_of(j + 1));
                 if (x == w.nq - 1) {
-                  umma_commit(empty + 8 * (kc % KS));
-                  if (j + 2 == w.j1) umma_commit(q_empty);  // the item's last use of Q
+                  commit(empty + 8 * (kc % KS));
+                  if (j + 2 == w.j1) commit(q_empty);  // the item's last use of Q
                 }
               }
             }
@@ -393,7 +421,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           ++items;
         }
         if (*abort_flag) {
-          umma_commit(drain);
+          commit(drain);
           settle(drain, 0);
         }
       }
@@ -539,12 +567,16 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         if (__any_sync(0xffffffffu, edge)) {
 #pragma unroll
           for (int i = 0; i < WP_SLABS; ++i) {
-            // elements of slab i: e > hi is past the row's last key; sk <= e < lo_e between its sinks and its window
+            // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
+            // window (selects, no branches: 128 short branches cost ten times the softmax itself)
             const int t0 = w.slab(u0 + i) * TILE;
-            const int hi = i < n ? lim - t0 : -1, lo_e = low - t0, sk = a.n_sink > t0 ? a.n_sink - t0 : 0;
+            const uint32_t vis =
+                i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
 #pragma unroll
-            for (int e = 0; e < TILE; ++e)
-              if (e > hi || (e < lo_e && e >= sk)) sv[i >> 1][(i & 1) * TILE + e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < TILE; ++e) {
+              uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
+              x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
+            }
           }
         }
         float mx8[8];
