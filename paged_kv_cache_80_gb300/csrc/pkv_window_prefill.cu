@@ -15,12 +15,12 @@
 // multiplies, which N = 64 does not.  A window makes items short (a window of 1,024 is 9 key tiles), so what surrounds them
 // counts: the grid is persistent, and loads, products and softmax of the next item start while this one's rows are written.
 //
-// Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 issues
-// the products; 10 zeroes V rows that no row sees (0 times whatever lies there must stay 0); 11 loads Q.  E4M3 pools:
-// 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16 operands.
+// Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 and 11
+// issue the products of A and of B; 10 loads Q and zeroes V rows that no row sees (0 times whatever lies there must
+// stay 0).  E4M3 pools: 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16.
 // TMEM: S of A and B (128 columns each; P overwrites its first 64), O of A and B from column 256 on.
-// Order of the tensor pipe: ..., P V(A, j), Q K(A, j + 1), P V(B, j), Q K(B, j + 1), ...: one thread issues all, so a
-// product sees the earlier ones done, and the arrival of S(j + 1) says that O holds P V(j).
+// A tile's products are issued by one thread and taken in order, ..., P V(j), Q K(j + 1), ...: S(j + 1) may go over
+// P(j), and its arrival says that O holds P V(j).
 //
 // Few items (a short chunk, one sequence) leave SMs idle: there a cluster of up to 8 CTAs takes one item, each a
 // range of its key tiles, and the partial (m, l, O) meet in shared memory.
@@ -53,11 +53,11 @@ struct WpCfg {
   static constexpr int STG_TILE = WP_KEYS * D;            // one K or V tile of E4M3 codes
   static constexpr int KS = KV8 ? 3 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
   static constexpr int FS = KV8 ? 4 : 0;                  // staging ring
-  static constexpr int BARS = 2 + 1 + 2 * KS + KS + 2 + 2 + 2 + 2 * 4 + 1;
+  static constexpr int BARS = 2 + 1 + 2 * KS + KS + 2 + 2 + 2 + 2 * 4 + 2 + 2;
   static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
   static constexpr int SMEM = 1024 + DATA + BARS * 8 + 16 + 64 + (WP_TBL + 1) * 4;
   // registers: the launch's share is 65,536 / THREADS (a multiple of 8: 168 and 128)
-  static constexpr int R_SOFTMAX = KV8 ? 184 : 208, R_CONTROL = KV8 ? 64 : 56, R_CONVERT = 72;
+  static constexpr int R_SOFTMAX = KV8 ? 184 : 208, R_CONTROL = KV8 ? 72 : 88, R_CONVERT = 72;
   static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 128 * R_CONVERT : 0) <= THREADS * (KV8 ? 128 : 168),
                 "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
   const uint32_t s_full = land + 8 * KS, p_full = s_full + 16, o_full = p_full + 16;  // per tile A, B
-  const uint32_t sf_full = o_full + 16, sf_empty = sf_full + 32, drain = sf_empty + 32;  // staging ring
+  const uint32_t sf_full = o_full + 16, sf_empty = sf_full + 32;     // staging ring
+  const uint32_t drain = sf_empty + 32, turn = drain + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar_p + C::BARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int32_t* wsum = reinterpret_cast<int32_t*>(tslot + 4);
@@ -151,22 +152,23 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_ready, 128);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int k = 0; k < KS; ++k) {
       mbar_init(full + 8 * k, KV8 ? 128 : 1);
-      mbar_init(empty + 8 * k, 1);
+      mbar_init(empty + 8 * k, 2);  // both tiles' products
       mbar_init(land + 8 * k, 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(s_full + 8 * x, 1);
       mbar_init(p_full + 8 * x, 128);
       mbar_init(o_full + 8 * x, 1);
+      mbar_init(drain + 8 * x, 1);
+      mbar_init(turn + 8 * x, 1);
     }
     for (int k = 0; k < FS; ++k) {
       mbar_init(sf_full + 8 * k, 1);
       mbar_init(sf_empty + 8 * k, 128);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -346,131 +348,129 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (!KV8 && (on_land >> slot & 1)) settle(land + 8 * slot, ~(land_par >> slot) & 1);
           else settle(r_full + 8 * slot, (k / RS) & 1);
         }
-    } else if (warp == 9) {
-      // ------------------------------------------------------------ the products
+    } else if (warp == 9 || warp == 11) {
+      // ------------------------------------------------------------ the products of tile X (9: A, 11: B)
       // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
       // divergent thread on its own needs some 140 cycles a product to bring its operands into uniform registers.
-      {
-        auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
-          return __all_sync(0xffffffffu, wait(bar, parity, where)) != 0;
-        };
-        const uint32_t idesc_o = umma_idesc_f16(BF16, 128, D, true);
-        uint32_t c = 0, items = 0, np = 0;  // ring position; items; bit x: parity of the P tiles taken of A, B
-        // operand descriptors: the first, and a step of the address field (16-byte units) from there on
-        const uint64_t q_desc = umma_desc_sw128(qs, 16, 1024), k_desc = umma_desc_sw128(ring, 16, 1024);
-        const uint64_t v_desc = umma_desc_sw128(ring, TILE * 128, 1024);
-        auto qk = [&](int x, uint32_t slot, int ns) {
-          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, ns * TILE, false);
-          const uint64_t qd = q_desc + x * (C::Q_TILE / 16), kd = k_desc + slot * (C::KV_TILE / 16);
-          if (!elect_one()) return;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) / 16;  // chunk; 16 elements along its 128-byte row
-            umma_ss(tmem + 128 * x, qd + off, kd + off, idesc_s, k > 0);
-          }
-          umma_commit(s_full + 8 * x);
-        };
-        auto pv = [&](int x, uint32_t slot, int ns, bool acc) {
-          const uint64_t vd = v_desc + slot * (C::KV_TILE / 16);
-          if (!elect_one()) return;
-#pragma unroll
-          for (int k = 0; k < WP_SLABS; ++k)
-            if (k < ns)
-              umma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o,
-                      acc || k > 0 ? 1u : 0u);
-        };
-        auto commit = [&](uint32_t bar) {
-          if (elect_one()) umma_commit(bar);
-        };
-        for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-          if (!get(idx, w, false)) continue;
-          if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
-          ok = wait_all(KV8 ? q_ready : q_full, items & 1, 200);
-          if (ok) ok = wait_all(full + 8 * (c % KS), (c / KS) & 1, 210);
-          if (!ok) break;
-          tc_fence_after();
-          for (int x = 0; x < w.nq; ++x) qk(x, c % KS, w.slabs_of(w.j0));
-          commit(empty + 8 * (c % KS));
-          ++c;
-          if (w.j1 - w.j0 == 1) commit(q_empty);
-          for (int j = w.j0; j < w.j1 && ok; ++j) {
-            const uint32_t vc = c, kc = c + 1;  // V(j), K(j + 1)
-            const bool more = j + 1 < w.j1;
-            for (int x = 0; x < w.nq && ok; ++x) {
-              ok = wait_all(p_full + 8 * x, np >> x & 1, 220);
-              if (ok && x == 0) ok = wait_all(full + 8 * (vc % KS), (vc / KS) & 1, 230);
-              if (!ok) break;
-              np ^= 1u << x;
-              tc_fence_after();
-              pv(x, vc % KS, w.slabs_of(j), j > w.j0);
-              if (!more) commit(o_full + 8 * x);
-              if (x == w.nq - 1) commit(empty + 8 * (vc % KS));
-              if (more) {
-                if (x == 0) ok = wait_all(full + 8 * (kc % KS), (kc / KS) & 1, 240);
-                if (!ok) break;
-                tc_fence_after();
-                qk(x, kc % KS, w.slabs_of(j + 1));
-                if (x == w.nq - 1) {
-                  commit(empty + 8 * (kc % KS));
-                  if (j + 2 == w.j1) commit(q_empty);  // the item's last use of Q
-                }
-              }
-            }
-            c += more ? 2 : 1;
-          }
-          ++items;
-        }
-        if (*abort_flag) {
-          commit(drain);
-          settle(drain, 0);
-        }
-      }
-    } else if (warp == 10) {
-      // ------------------------------------------------------------ V rows hidden from every row of the item
-      if (!KV8) {
-        uint32_t c = 0, uses = 0;  // ring position; bit k: parity of `land` uses of slot k
-        for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-          if (!get(idx, w, false)) continue;
-          for (int j = w.j0; j < w.j1 && ok; ++j, c += 2) {
-            if (!w.zeroes(j)) continue;
-            const uint32_t slot = (c + 1) % KS;
-            if (lane == 0) ok = wait(land + 8 * slot, uses >> slot & 1, 300);
-            ok = warp_ok(ok);
-            if (!ok) break;
-            uses ^= 1u << slot;
-            uint8_t* vt = ring_p + slot * C::KV_TILE;
-            for (int i = 0; i < w.slabs_of(j); ++i) {
-              const int u = j * WP_SLABS + i;
-              if (!w.ragged(u)) continue;
-              const int t0 = w.slab(u) * TILE;
-              for (int k = lane; k < TILE * 8 * C::NCH; k += 32) {  // 16-byte pieces of the slab
-                const int r = k / (8 * C::NCH), p = k % (8 * C::NCH);
-                if (w.hidden(t0 + r))
-                  *reinterpret_cast<int4*>(vt + i * (C::NCH * TILE * 128) + p / 8 * (TILE * 128) + r * 128 + p % 8 * 16) =
-                      make_int4(0, 0, 0, 0);
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + 8 * slot);
-          }
-        }
-      }
-    } else if (lane == 0) {
-      // ------------------------------------------------------------ Q
-      uint32_t items = 0;
+      // A and B take turns, (P V, Q K) of one, then of the other, so that S of A arrives while B's products run and the
+      // two softmaxes stay half a period apart; issued side by side, the products of both end together, and then both
+      // softmaxes run while the tensor cores wait.  A tile without rows (nq = 1) has its turns all the same.
+      const int X = warp == 9 ? 0 : 1;
+      const uint32_t s_tm = tmem + 128 * X, o_tm = tmem + 256 + 128 * X;
+      const uint32_t idesc_o = umma_idesc_f16(BF16, 128, D, true);
+      // operand descriptors: the first, and a step of the address field (16-byte units) from there on
+      const uint64_t q_desc = umma_desc_sw128(qs + X * C::Q_TILE, 16, 1024), k_desc = umma_desc_sw128(ring, 16, 1024);
+      const uint64_t v_desc = umma_desc_sw128(ring, TILE * 128, 1024);
+      auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
+        return __all_sync(0xffffffffu, wait(bar, parity, where)) != 0;
+      };
+      auto commit = [&](uint32_t bar) {
+        if (elect_one()) umma_commit(bar);
+      };
+      uint32_t c = 0, items = 0, np = 0, turns = 0;  // ring position; items; P tiles taken; turns had
       for (int64_t idx = begin; idx < n_items && ok; idx += step) {
         if (!get(idx, w, false) || w.j0 == w.j1) continue;
-        if (items > 0) ok = wait(q_empty, (items - 1) & 1, 400);
-        if (!ok) break;
-        fence_proxy_async();
-        mbar_arrive_expect_tx(q_full, w.nq * G * QB * D * 2);  // G * QB rows a tile (126 for G = 3)
-        for (int x = 0; x < w.nq; ++x)
-          for (int h = 0; h < C::NCH; ++h)
-            tma_load_3d(qs + x * C::Q_TILE + h * 16384, &tmq, 64 * h, w.g * G, w.qbeg + w.i0 + x * QB, q_full);
-        ++items;
+        const bool live = X < w.nq;
+        ok = wait_all(KV8 ? q_ready : q_full, items++ & 1, 200);
+        for (int j = w.j0 - 1; j < w.j1 && ok; ++j) {  // P V of tile j, then Q K of tile j + 1
+          // everything is waited for before the turn: within it the products follow each other without a gap
+          const bool has_pv = j >= w.j0, has_qk = j + 1 < w.j1;
+          const uint32_t vs = c % KS, ks = (c + has_pv) % KS;
+          if (has_pv) {
+            ok = wait_all(full + 8 * vs, (c / KS) & 1, 210);
+            ++c;
+          }
+          if (ok && has_qk) {
+            ok = wait_all(full + 8 * ks, (c / KS) & 1, 220);
+            ++c;
+          }
+          if (ok && has_pv && live) ok = wait_all(p_full + 8 * X, np++ & 1, 230);
+          if (ok && (X == 1 || turns > 0)) ok = wait_all(turn + 8 * X, (turns - 1 + X) & 1, 240);
+          if (!ok) break;
+          ++turns;
+          tc_fence_after();
+          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * (C::KV_TILE / 16);
+          const int nv = has_pv ? w.slabs_of(j) : 0;
+          const uint32_t acc = j > w.j0 ? 1u : 0u;
+          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, has_qk ? w.slabs_of(j + 1) * TILE : TILE, false);
+          if (elect_one()) {
+            if (live) {
+#pragma unroll
+              for (int k = 0; k < WP_SLABS; ++k)
+                if (k < nv) umma_ts(o_tm, s_tm + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, k > 0 ? 1u : acc);
+              if (has_qk) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) / 16;  // chunk; 16 elements along its row
+                  // the other tile's thread is let go two products early, which hides its start
+                  if (k == D / 16 - 2) mbar_arrive(turn + 8 * (1 - X));
+                  umma_ss(s_tm, q_desc + off, kd + off, idesc_s, k > 0);
+                }
+                umma_commit(s_full + 8 * X);
+              } else {
+                mbar_arrive(turn + 8 * (1 - X));
+                umma_commit(o_full + 8 * X);
+              }
+              // this tile's use of the operands is over once its products so far are done
+              if (has_pv) umma_commit(empty + 8 * vs);
+              if (has_qk) umma_commit(empty + 8 * ks);
+              if (j + 2 == w.j1) umma_commit(q_empty);
+            } else {
+              mbar_arrive(turn + 8 * (1 - X));
+              if (has_pv) mbar_arrive(empty + 8 * vs);
+              if (has_qk) mbar_arrive(empty + 8 * ks);
+              if (j + 2 == w.j1) mbar_arrive(q_empty);
+            }
+          }
+          __syncwarp();
+        }
       }
-      if (*abort_flag && items > 0) settle(q_full, (items - 1) & 1);
+      if (*abort_flag) {
+        commit(drain + 8 * X);
+        settle(drain + 8 * X, 0);
+      }
+    } else {
+      // ------------------------------------------------------------ Q; V rows hidden from every row of the item
+      uint32_t c = 0, uses = 0, items = 0;  // ring position; bit k: parity of `land` uses of slot k; items
+      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
+        if (!get(idx, w, false) || w.j0 == w.j1) continue;
+        if (lane == 0) {
+          if (items > 0) ok = wait(q_empty, (items - 1) & 1, 400);
+          if (ok) {
+            fence_proxy_async();
+            mbar_arrive_expect_tx(q_full, w.nq * G * QB * D * 2);  // G * QB rows a tile (126 for G = 3)
+            for (int x = 0; x < w.nq; ++x)
+              for (int h = 0; h < C::NCH; ++h)
+                tma_load_3d(qs + x * C::Q_TILE + h * 16384, &tmq, 64 * h, w.g * G, w.qbeg + w.i0 + x * QB, q_full);
+            ++items;
+          }
+        }
+        ok = warp_ok(ok);
+        for (int j = w.j0; j < w.j1 && ok && !KV8; ++j, c += 2) {  // (E4M3: the conversion writes the zeros)
+          if (!w.zeroes(j)) continue;
+          const uint32_t slot = (c + 1) % KS;
+          if (lane == 0) ok = wait(land + 8 * slot, uses >> slot & 1, 300);
+          ok = warp_ok(ok);
+          if (!ok) break;
+          uses ^= 1u << slot;
+          uint8_t* vt = ring_p + slot * C::KV_TILE;
+          for (int i = 0; i < w.slabs_of(j); ++i) {
+            const int u = j * WP_SLABS + i;
+            if (!w.ragged(u)) continue;
+            const int t0 = w.slab(u) * TILE;
+            for (int k = lane; k < TILE * 8 * C::NCH; k += 32) {  // 16-byte pieces of the slab
+              const int r = k / (8 * C::NCH), p = k % (8 * C::NCH);
+              if (w.hidden(t0 + r))
+                *reinterpret_cast<int4*>(vt + i * (C::NCH * TILE * 128) + p / 8 * (TILE * 128) + r * 128 + p % 8 * 16) =
+                    make_int4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + 8 * slot);
+        }
+      }
+      if (*abort_flag && lane == 0 && items > 0) settle(q_full, (items - 1) & 1);
     }
   } else if (warp >= 12) {
     // -------------------------------------------------------------- E4M3: q and the staged codes to binary16
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       if (w.j0 < w.j1) {
         ok = __all_sync(0xffffffffu, wait(o_full + 8 * X, no & 1, 700));
         // a cluster's partial goes over the operands: not before the products of the other tile are done, too
-        if (ok && csize > 1 && X == 0 && w.nq == 2) ok = __all_sync(0xffffffffu, wait(o_full + 8, 0, 710));
+        if (ok && csize > 1 && w.nq == 2) ok = __all_sync(0xffffffffu, wait(o_full + 8 * (1 - X), 0, 710));
         if (!ok) break;
         ++no;
         tc_fence_after();
