@@ -41,7 +41,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int WP_KEYS = 128, WP_SLABS = WP_KEYS / TILE;
+constexpr int WP_KEYS = 64, WP_SLABS = WP_KEYS / TILE;
 constexpr int WP_TBL = 384;  // entries of the table that finds an item's sequence
 
 template <bool KV8, int D>
@@ -51,9 +51,9 @@ struct WpCfg {
   static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
   static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile as an operand (16-bit)
   static constexpr int STG_TILE = WP_KEYS * D;            // one K or V tile of E4M3 codes
-  static constexpr int KS = KV8 ? 3 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
-  static constexpr int FS = KV8 ? 4 : 0;                  // staging ring
-  static constexpr int BARS = 2 + 1 + 2 * KS + KS + 2 + 2 + 2 + 2 * 4 + 2 + 2;
+  static constexpr int KS = KV8 ? 6 : (D == 64 ? 16 : 10);  // operand ring: K and V tiles in turn
+  static constexpr int FS = KV8 ? 8 : 0;                  // staging ring
+  static constexpr int BARS = 3 + 3 * KS + 4 + 4 + 3 * 2 + 2 * FS;
   static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
   static constexpr int SMEM = 1024 + DATA + BARS * 8 + 16 + 64 + (WP_TBL + 1) * 4;
   // registers: the launch's share is 65,536 / THREADS (a multiple of 8: 168 and 128)
@@ -78,6 +78,23 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r != 0;
+}
+
+// two binary32 products and sums, or sums, an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, z, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 r, x, y, z;\nmov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // the lowest n of 16 bits
@@ -124,7 +141,6 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     prefill_win_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const DecodeArgs a, const int32_t* __restrict__ q_off,
                        int32_t max_q, int32_t csize, int64_t most_items) {
-  static_assert(WP_KEYS * 128 == 16384, "Q and K chunks are alike");
   using C = WpCfg<KV8, D>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // operand type of the products
   using TP = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -141,9 +157,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   uint8_t* bar_p = base + C::DATA;
   const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
-  const uint32_t s_full = land + 8 * KS, p_full = s_full + 16, o_full = p_full + 16;  // per tile A, B
-  const uint32_t sf_full = o_full + 16, sf_empty = sf_full + 32;     // staging ring
-  const uint32_t drain = sf_empty + 32, turn = drain + 16;
+  // per tile A, B: S of an even, odd key tile; P likewise; P V done; the item's O done; after an abort
+  const uint32_t s_full = land + 8 * KS, p_full = s_full + 32, o_done = p_full + 32, o_full = o_done + 16;
+  const uint32_t drain = o_full + 16, sf_full = drain + 16, sf_empty = sf_full + 64;  // staging ring
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar_p + C::BARS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int32_t* wsum = reinterpret_cast<int32_t*>(tslot + 4);
@@ -151,23 +167,25 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_ready, 128);
+    mbar_init(q_ready, 4);  // one arrival a warp
     mbar_init(q_empty, 2);
     for (int k = 0; k < KS; ++k) {
-      mbar_init(full + 8 * k, KV8 ? 128 : 1);
+      mbar_init(full + 8 * k, KV8 ? 4 : 1);
       mbar_init(empty + 8 * k, 2);  // both tiles' products
       mbar_init(land + 8 * k, 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(s_full + 8 * x, 1);
-      mbar_init(p_full + 8 * x, 128);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(s_full + 16 * x + 8 * b, 1);
+        mbar_init(p_full + 16 * x + 8 * b, 4);
+      }
+      mbar_init(o_done + 8 * x, 1);
       mbar_init(o_full + 8 * x, 1);
       mbar_init(drain + 8 * x, 1);
-      mbar_init(turn + 8 * x, 1);
     }
     for (int k = 0; k < FS; ++k) {
       mbar_init(sf_full + 8 * k, 1);
-      mbar_init(sf_empty + 8 * k, 128);
+      mbar_init(sf_empty + 8 * k, 4);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -302,7 +320,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           }
           return ((blk * a.L + a.layer) * a.H_kv + w.g) * a.B + (t0 - lb * a.B);
         };
-        constexpr int TPG = 32 / WP_SLABS;  // tiles a group of 32 slabs
+        constexpr int TPG = 32 / WP_SLABS;  // key tiles a group of 32 slabs
         int row = row_of(w.j0 * WP_SLABS + lane);
         int next = w.j0 + TPG < w.j1 ? row_of((w.j0 + TPG) * WP_SLABS + lane) : 0;
         for (int j = w.j0; j < w.j1 && ok; ++j) {
@@ -352,9 +370,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // ------------------------------------------------------------ the products of tile X (9: A, 11: B)
       // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
       // divergent thread on its own needs some 140 cycles a product to bring its operands into uniform registers.
-      // A and B take turns, (P V, Q K) of one, then of the other, so that S of A arrives while B's products run and the
-      // two softmaxes stay half a period apart; issued side by side, the products of both end together, and then both
-      // softmaxes run while the tensor cores wait.  A tile without rows (nq = 1) has its turns all the same.
+      // S has two buffers, so that Q K of the next key tile runs while this one's softmax does, and a softmax finds its
+      // scores ready.  A tile without rows (nq = 1) takes its part in the operand ring all the same.
       const int X = warp == 9 ? 0 : 1;
       const uint32_t s_tm = tmem + 128 * X, o_tm = tmem + 256 + 128 * X;
       const uint32_t idesc_o = umma_idesc_f16(BF16, 128, D, true);
@@ -367,63 +384,69 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       auto commit = [&](uint32_t bar) {
         if (elect_one()) umma_commit(bar);
       };
-      uint32_t c = 0, items = 0, np = 0, turns = 0;  // ring position; items; P tiles taken; turns had
+      uint32_t c = 0, items = 0, ns_ = 0, np = 0;  // ring position of the item's first K; items; S and P tiles so far
       for (int64_t idx = begin; idx < n_items && ok; idx += step) {
         if (!get(idx, w, false) || w.j0 == w.j1) continue;
         const bool live = X < w.nq;
+        const int nt = w.j1 - w.j0;
         ok = wait_all(KV8 ? q_ready : q_full, items++ & 1, 200);
-        for (int j = w.j0 - 1; j < w.j1 && ok; ++j) {  // P V of tile j, then Q K of tile j + 1
-          // everything is waited for before the turn: within it the products follow each other without a gap
-          const bool has_pv = j >= w.j0, has_qk = j + 1 < w.j1;
-          const uint32_t vs = c % KS, ks = (c + has_pv) % KS;
-          if (has_pv) {
-            ok = wait_all(full + 8 * vs, (c / KS) & 1, 210);
-            ++c;
-          }
-          if (ok && has_qk) {
-            ok = wait_all(full + 8 * ks, (c / KS) & 1, 220);
-            ++c;
-          }
-          if (ok && has_pv && live) ok = wait_all(p_full + 8 * X, np++ & 1, 230);
-          if (ok && (X == 1 || turns > 0)) ok = wait_all(turn + 8 * X, (turns - 1 + X) & 1, 240);
-          if (!ok) break;
-          ++turns;
+        // S of the item's i-th key tile (its K is at ring position c + 2 i)
+        auto qk = [&](int i) -> bool {
+          const uint32_t at = c + 2 * i, slot = at % KS;
+          if (!wait_all(full + 8 * slot, (at / KS) & 1, 210)) return false;
           tc_fence_after();
-          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * (C::KV_TILE / 16);
-          const int nv = has_pv ? w.slabs_of(j) : 0;
-          const uint32_t acc = j > w.j0 ? 1u : 0u;
-          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, has_qk ? w.slabs_of(j + 1) * TILE : TILE, false);
+          const uint64_t kd = k_desc + slot * (C::KV_TILE / 16);
+          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, w.slabs_of(w.j0 + i) * TILE, false);
+          const uint32_t b = ns_ & 1;
+          if (elect_one()) {
+            if (live) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)  // 64-wide chunk; 16 elements along its 128-byte row
+                umma_ss(s_tm + 64 * b, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
+                        kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
+              umma_commit(s_full + 16 * X + 8 * b);
+              umma_commit(empty + 8 * slot);  // this tile's use of the operand is over once its products are done
+              if (i + 1 == nt) umma_commit(q_empty);
+            } else {
+              mbar_arrive(empty + 8 * slot);
+              if (i + 1 == nt) mbar_arrive(q_empty);
+            }
+          }
+          __syncwarp();
+          ++ns_;
+          return true;
+        };
+        auto pv = [&](int i) -> bool {
+          const uint32_t at = c + 2 * i + 1, slot = at % KS, b = np & 1;
+          if (!wait_all(full + 8 * slot, (at / KS) & 1, 220)) return false;
+          if (live && !wait_all(p_full + 16 * X + 8 * b, (np >> 1) & 1, 230)) return false;
+          tc_fence_after();
+          const uint64_t vd = v_desc + slot * (C::KV_TILE / 16);
+          const int n = w.slabs_of(w.j0 + i);
           if (elect_one()) {
             if (live) {
 #pragma unroll
               for (int k = 0; k < WP_SLABS; ++k)
-                if (k < nv) umma_ts(o_tm, s_tm + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, k > 0 ? 1u : acc);
-              if (has_qk) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                  const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) / 16;  // chunk; 16 elements along its row
-                  // the other tile's thread is let go two products early, which hides its start
-                  if (k == D / 16 - 2) mbar_arrive(turn + 8 * (1 - X));
-                  umma_ss(s_tm, q_desc + off, kd + off, idesc_s, k > 0);
-                }
-                umma_commit(s_full + 8 * X);
-              } else {
-                mbar_arrive(turn + 8 * (1 - X));
-                umma_commit(o_full + 8 * X);
-              }
-              // this tile's use of the operands is over once its products so far are done
-              if (has_pv) umma_commit(empty + 8 * vs);
-              if (has_qk) umma_commit(empty + 8 * ks);
-              if (j + 2 == w.j1) umma_commit(q_empty);
+                if (k < n)
+                  umma_ts(o_tm, s_tm + 64 * b + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+              umma_commit(o_done + 8 * X);
+              if (i + 1 == nt) umma_commit(o_full + 8 * X);
+              umma_commit(empty + 8 * slot);
             } else {
-              mbar_arrive(turn + 8 * (1 - X));
-              if (has_pv) mbar_arrive(empty + 8 * vs);
-              if (has_qk) mbar_arrive(empty + 8 * ks);
-              if (j + 2 == w.j1) mbar_arrive(q_empty);
+              mbar_arrive(empty + 8 * slot);
             }
           }
           __syncwarp();
+          ++np;
+          return true;
+        };
+        if (ok) ok = qk(0);
+        for (int i = 0; i < nt && ok; ++i) {
+          if (i + 1 < nt) ok = qk(i + 1);
+          if (ok) ok = pv(i);
         }
+        c += 2 * nt;
+        if (!live) ns_ -= nt, np -= nt;  // no S or P of this tile
       }
       if (*abort_flag) {
         commit(drain + 8 * X);
@@ -493,12 +516,13 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           reinterpret_cast<uint4*>(base)[k] = v;
         }
         fence_proxy_async();
-        mbar_arrive(q_ready);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
         ++items;
         for (int j = w.j0; j < w.j1 && ok; ++j)
           for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
-            const uint32_t f = c % 4, slot = c % KS;
-            bool here = wait(sf_full + 8 * f, (c / 4) & 1, 510);
+            const uint32_t f = c % 8, slot = c % KS;
+            bool here = wait(sf_full + 8 * f, (c / 8) & 1, 510);
             if (here && c >= KS) here = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 520);
             ok = __all_sync(0xffffffffu, here);
             if (!ok) break;
@@ -525,13 +549,16 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               cvt(v.w, o1.z, o1.w);
               if (zero && w.hidden(w.slab(j * WP_SLABS + i) * TILE + rr)) o0 = o1 = make_uint4(0, 0, 0, 0);
               uint8_t* p = kv == 0 ? dst + cc * (WP_KEYS * 128) + (i * TILE + rr) * 128
-                                   : dst + i * 4096 + cc * 2048 + rr * 128;
+                                   : dst + i * (2 * TILE * 128) + cc * (TILE * 128) + rr * 128;
               *reinterpret_cast<uint4*>(p + ((t ^ sw) << 4)) = o0;
               *reinterpret_cast<uint4*>(p + (((t + 1) ^ sw) << 4)) = o1;
             }
             fence_proxy_async();
-            mbar_arrive(full + 8 * slot);
-            mbar_arrive(sf_empty + 8 * f);
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(full + 8 * slot);
+              mbar_arrive(sf_empty + 8 * f);
+            }
           }
       }
     }
@@ -540,9 +567,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::R_SOFTMAX));
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
+    const uint32_t o_addr = lane_addr + 256 + 128 * X;
     const float sl = a.scale_log2;
-    uint32_t ns_ = 0, no = 0;  // S tiles and outputs taken
+    uint32_t n_s = 0, no = 0;  // S tiles and outputs taken
     for (int64_t idx = begin; idx < n_items && ok; idx += step) {
       if (!get(idx, w, X == 0 && tid == 0 && rank == 0)) continue;
       if (X >= w.nq) continue;
@@ -551,49 +578,53 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
       float m = -INFINITY, l = 0.f;
-      for (int j = w.j0; j < w.j1 && ok; ++j) {
-        ok = __all_sync(0xffffffffu, wait(s_full + 8 * X, ns_ & 1, 600));
+      for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
+        const uint32_t b = n_s & 1, s_addr = lane_addr + 128 * X + 64 * b;
+        ok = __all_sync(0xffffffffu, wait(s_full + 16 * X + 8 * b, (n_s >> 1) & 1, 600));
         if (!ok) break;
-        ++ns_;
         tc_fence_after();
-        uint32_t sv[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, sv[c]);
-        tmem_ld_wait();
+        uint32_t sv[2][32];
+        tmem_ld32(s_addr, sv[0]);
+        tmem_ld32(s_addr + 32, sv[1]);
         // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
         const int u0 = j * WP_SLABS, n = w.slabs_of(j);
         const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
-        const bool edge = n < WP_SLABS || t_last > lim || t_first < low;
-        if (__any_sync(0xffffffffu, edge)) {
+        const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
+        tmem_ld_wait();
+        if (edge) {
 #pragma unroll
           for (int i = 0; i < WP_SLABS; ++i) {
             // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
-            // window (selects, no branches: 128 short branches cost ten times the softmax itself)
+            // window (selects, no branches: 64 short branches cost ten times the softmax itself)
             const int t0 = w.slab(u0 + i) * TILE;
-            const uint32_t vis =
-                i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+            const uint32_t vis = i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+            if (__any_sync(0xffffffffu, vis != 0xffffu)) {
 #pragma unroll
-            for (int e = 0; e < TILE; ++e) {
-              uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
-              x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
+              for (int e = 0; e < TILE; ++e) {
+                uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
+                x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
+              }
             }
           }
         }
-        float mx8[8];
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < 8; ++t) mx8[t] = -INFINITY;
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int e = 0; e < 32; e += 8)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(sv[c][e]));
-        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+            for (int t = 0; t < 4; ++t)
+              mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(sv[c][e + t]), __uint_as_float(sv[c][e + t + 4])));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const float m_new = fmaxf(m, mx * sl);
         // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
-        // l and O so far are rescaled; S(j) is here, so O holds P V(j - 1)
+        // l and O so far are rescaled, once O holds P V(j - 1)
         if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
           const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
           if (j > w.j0) {
+            ok = __all_sync(0xffffffffu, wait(o_done + 8 * X, (n_s - 1) & 1, 610));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -610,25 +641,28 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         // P = 2^(scale s - m), 16-bit, two keys a column, over the S just read; a row that has seen no key yet
         // keeps m = -inf, and 0 stands in for it
         const float neg_m = m == -INFINITY ? 0.f : -m;
-        float ls8[8];
+        float2 ls[4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) ls8[t] = 0.f;
+        for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(sv[c][2 * e]), sl, neg_m));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(sv[c][2 * e + 1]), sl, neg_m));
-            ls8[e & 7] += p0 + p1;
-            pw[e] = pack2<TP>(p0, p1);
+            float2 p = fma2(make_float2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])),
+                            make_float2(sl, sl), make_float2(neg_m, neg_m));
+            p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
+            ls[e & 3] = add2(ls[e & 3], p);
+            pw[e] = pack2<TP>(p.x, p.y);
           }
           tmem_st16(s_addr + 16 * c, pw);
         }
-        l += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
+        const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+        l += l2.x + l2.y;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_full + 8 * X);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 16 * X + 8 * b);
       }
       if (!ok) break;
       if (w.j0 < w.j1) {
