@@ -42,24 +42,25 @@ namespace pkv {
 namespace {
 
 constexpr int WP_KEYS = 64, WP_SLABS = WP_KEYS / TILE;
-constexpr int WP_TBL = 384;  // entries of the table that finds an item's sequence
+constexpr int WP_TBL = 256;  // entries of the table that finds an item's sequence
 
 template <bool KV8, int D>
 struct WpCfg {
-  static constexpr int THREADS = KV8 ? 512 : 384;
+  static constexpr int THREADS = KV8 ? 640 : 384;
   static constexpr int NCH = D / 64;                      // 64-wide chunks of d (128 bytes, the swizzle's width)
   static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
   static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile as an operand (16-bit)
   static constexpr int STG_TILE = WP_KEYS * D;            // one K or V tile of E4M3 codes
   static constexpr int KS = KV8 ? 6 : (D == 64 ? 16 : 10);  // operand ring: K and V tiles in turn
   static constexpr int FS = KV8 ? 8 : 0;                  // staging ring
-  static constexpr int BARS = 3 + 3 * KS + 4 + 4 + 3 * 2 + 2 * FS;
+  static constexpr int BARS = 3 + 3 * KS + 4 + 4 + 3 * 2 + 4 + 2 * FS;
+  static constexpr int READERS = THREADS / 32 - 1;        // warps that follow the items
   static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
-  static constexpr int SMEM = 1024 + DATA + BARS * 8 + 16 + 64 + (WP_TBL + 1) * 4;
-  // registers: the launch's share is 65,536 / THREADS (a multiple of 8: 168 and 128)
-  static constexpr int R_SOFTMAX = KV8 ? 184 : 208, R_CONTROL = KV8 ? 72 : 88, R_CONVERT = 72;
-  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 128 * R_CONVERT : 0) <= THREADS * (KV8 ? 128 : 168),
-                "register split");
+  static constexpr int SMEM = 1024 + DATA + (BARS + 1) * 8 + 16 + 2 * 64 + 96 + (WP_TBL + 1) * 4;
+  // registers: the launch's share is 65,536 / THREADS rounded down to a multiple of 8
+  static constexpr int R_LAUNCH = KV8 ? 96 : 168;
+  static constexpr int R_SOFTMAX = KV8 ? 160 : 208, R_CONTROL = KV8 ? 64 : 88, R_CONVERT = 48;
+  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 256 * R_CONVERT : 0) <= THREADS * R_LAUNCH, "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -103,6 +104,18 @@ __device__ __forceinline__ uint32_t below(int n) {
   return (1u << k) - 1u;
 }
 
+// four E4M3 codes to binary16 (exact), and two bfloat16 rounded to binary16, the first of each pair low
+__device__ __forceinline__ void f16_of_e4m3(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t x) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -113,14 +126,15 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// One item: where its rows and keys are.
-struct Item {
+// One item: where its rows and keys are (16 words: it travels through shared memory).
+struct __align__(16) Item {
   int32_t s, g;
   int32_t qbeg, i0, i1, nq;              // chunk's first row; its queries i0 .. i1 - 1; tiles with rows (1, 2)
   int32_t P, nkeys;                      // position of query 0; keys up to the last query
   int32_t sink_end, lo;                  // a key t is hidden from every row if sink_end <= t < lo
   int32_t sink_slabs, first, nslab;      // the slab list: 0 .. sink_slabs - 1, then from `first` on
   int32_t j0, j1;                        // this CTA's key tiles
+  int32_t work;                          // 0: no item (any more)
   __device__ __forceinline__ int32_t slab(int32_t u) const { return u < sink_slabs ? u : first + u - sink_slabs; }
   __device__ __forceinline__ int32_t slabs_of(int32_t j) const { return min(WP_SLABS, nslab - j * WP_SLABS); }
   __device__ __forceinline__ bool hidden(int32_t t) const { return t >= nkeys || (t >= sink_end && t < lo); }
@@ -159,15 +173,18 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
   // per tile A, B: S of an even, odd key tile; P likewise; P V done; the item's O done; after an abort
   const uint32_t s_full = land + 8 * KS, p_full = s_full + 32, o_done = p_full + 32, o_full = o_done + 16;
-  const uint32_t drain = o_full + 16, sf_full = drain + 16, sf_empty = sf_full + 64;  // staging ring
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar_p + C::BARS * 8);
+  const uint32_t drain = o_full + 16, sf_full = drain + 16, sf_empty = sf_full + 8 * FS;  // staging ring
+  const uint32_t it_full = sf_full + 16 * FS, it_empty = it_full + 16;  // items, two places
+  uint8_t* tail_p = bar_p + (C::BARS + 1) / 2 * 16;
+  Item* items_p = reinterpret_cast<Item*>(tail_p);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(tail_p + 2 * sizeof(Item));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int32_t* wsum = reinterpret_cast<int32_t*>(tslot + 4);
-  int32_t* pre = wsum + 16;  // [groups + 1]: query-block pairs of the sequences before a group of them
+  int32_t* pre = wsum + 24;  // [groups + 1]: query-block pairs of the sequences before a group of them
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_ready, 4);  // one arrival a warp
+    mbar_init(q_ready, 8);  // one arrival a warp
     mbar_init(q_empty, 2);
     for (int k = 0; k < KS; ++k) {
       mbar_init(full + 8 * k, KV8 ? 4 : 1);
@@ -186,6 +203,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     for (int k = 0; k < FS; ++k) {
       mbar_init(sf_full + 8 * k, 1);
       mbar_init(sf_empty + 8 * k, 4);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(it_full + 8 * k, 1);
+      mbar_init(it_empty + 8 * k, C::READERS);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -228,7 +249,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   const int64_t step = csize > 1 ? n_items : gridDim.x;  // a cluster takes one item
   const int64_t begin = csize > 1 ? blockIdx.x / csize : blockIdx.x;
 
-  // item idx; false for one without work.  Every role calls it for the same items; `record` reports bad values.
+  // item idx; false for one without work.  `record` reports bad values.
   auto get = [&](int64_t idx, Item& w, bool record) __attribute__((always_inline)) -> bool {
     int lo = 0, hi = groups - 1;
     while (lo < hi) {
@@ -266,8 +287,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     w.first = max(w.sink_slabs, v.lo / TILE);
     w.nslab = w.sink_slabs + (w.nkeys + TILE - 1) / TILE - w.first;
     const int nt = (w.nslab + WP_SLABS - 1) / WP_SLABS;
-    w.j0 = static_cast<int>(static_cast<int64_t>(nt) * rank / csize);
-    w.j1 = static_cast<int>(static_cast<int64_t>(nt) * (rank + 1) / csize);
+    w.j0 = csize > 1 ? static_cast<int>(static_cast<int64_t>(nt) * rank / csize) : 0;
+    w.j1 = csize > 1 ? static_cast<int>(static_cast<int64_t>(nt) * (rank + 1) / csize) : nt;
+    w.work = 1;
     return true;
   };
 
@@ -292,6 +314,17 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     }
   };
   auto warp_ok = [&](bool ok) { return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0; };
+  // The next item, looked up by warp 10 while the last ones were at work; false after the last (or an abort).
+  uint32_t n_it = 0;
+  auto next_item = [&](Item& w) -> bool {
+    const uint32_t k = n_it & 1;
+    if (!__all_sync(0xffffffffu, wait(it_full + 8 * k, (n_it >> 1) & 1, 900))) return false;
+    w = items_p[k];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(it_empty + 8 * k);
+    ++n_it;
+    return w.work != 0;
+  };
 
   Item w;
   bool ok = true;
@@ -308,8 +341,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       uint32_t c = 0;  // tiles loaded so far
       uint32_t on_land = 0;  // of the last RS tiles, those whose bytes arrive at `land` (bit c % RS)
       uint32_t land_par = 0;  // bit k: parity of the uses of `land` slot k
-      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-        if (!get(idx, w, false)) continue;
+      while (ok && next_item(w)) {
         auto row_of = [&](int u) -> int {
           if (u >= w.nslab) return 0;
           const int t0 = w.slab(u) * TILE, lb = t0 / a.B;
@@ -385,8 +417,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         if (elect_one()) umma_commit(bar);
       };
       uint32_t c = 0, items = 0, ns_ = 0, np = 0;  // ring position of the item's first K; items; S and P tiles so far
-      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-        if (!get(idx, w, false) || w.j0 == w.j1) continue;
+      while (ok && next_item(w)) {
+        if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
         const bool live = X < w.nq;
         const int nt = w.j1 - w.j0;
         ok = wait_all(KV8 ? q_ready : q_full, items++ & 1, 200);
@@ -455,8 +487,28 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     } else {
       // ------------------------------------------------------------ Q; V rows hidden from every row of the item
       uint32_t c = 0, uses = 0, items = 0;  // ring position; bit k: parity of `land` uses of slot k; items
-      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-        if (!get(idx, w, false) || w.j0 == w.j1) continue;
+      int64_t idx = begin;
+      auto publish = [&](uint32_t n) -> bool {  // the n-th item (or the end) into its place
+        bool room = true;
+        if (lane == 0 && n >= 2) room = wait(it_empty + 8 * (n & 1), ((n >> 1) - 1) & 1, 910);
+        if (!warp_ok(room)) return false;
+        w.work = 0;
+        for (; idx < n_items && !w.work; idx += step)
+          if (!get(idx, w, lane == 0 && rank == 0)) w.work = 0;
+        if (lane == 0) {
+          items_p[n & 1] = w;
+          mbar_arrive(it_full + 8 * (n & 1));
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = publish(0);
+      for (uint32_t n = 0; ok; ++n) {
+        if (!items_p[n & 1].work) break;
+        ok = publish(n + 1);  // one ahead of what the others work on
+        if (!ok) break;
+        w = items_p[n & 1];
+        if (w.j0 == w.j1) continue;
         if (lane == 0) {
           if (items > 0) ok = wait(q_empty, (items - 1) & 1, 400);
           if (ok) {
@@ -498,31 +550,28 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   } else if (warp >= 12) {
     // -------------------------------------------------------------- E4M3: q and the staged codes to binary16
     if constexpr (KV8) {
+      // warps 12-15: q of tile A, then the K tiles; 16-19: q of B, the V tiles
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_CONVERT));
-      const int r = tid & 127;
-      uint32_t c = 0, items = 0;
-      for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-        if (!get(idx, w, false) || w.j0 == w.j1) continue;
-        ok = __all_sync(0xffffffffu, wait(q_full, items & 1, 500));
+      const int r = tid & 127, kv = warp >= 16;
+      uint32_t c = kv, items = 0;
+      while (ok && next_item(w)) {
+        if (w.j0 == w.j1) continue;
+        ok = __all_sync(0xffffffffu, wait(q_full, items++ & 1, 500));
         if (!ok) break;
-        for (int k = r; k < w.nq * C::Q_TILE / 16; k += 128) {
-          uint4 v = reinterpret_cast<uint4*>(base)[k];
-          uint32_t* p = &v.x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(p[e] << 16), __uint_as_float(p[e] & 0xffff0000u));
-            p[e] = *reinterpret_cast<const uint32_t*>(&h);
+        uint4* qt = reinterpret_cast<uint4*>(base + kv * C::Q_TILE);
+        if (kv < w.nq)
+#pragma unroll 4
+          for (int k = r; k < C::Q_TILE / 16; k += 128) {
+            uint4 v = qt[k];
+            v = make_uint4(f16_of_bf16(v.x), f16_of_bf16(v.y), f16_of_bf16(v.z), f16_of_bf16(v.w));
+            qt[k] = v;
           }
-          reinterpret_cast<uint4*>(base)[k] = v;
-        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        ++items;
-        for (int j = w.j0; j < w.j1 && ok; ++j)
-          for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
-            const uint32_t f = c % 8, slot = c % KS;
-            bool here = wait(sf_full + 8 * f, (c / 8) & 1, 510);
+        for (int j = w.j0; j < w.j1 && ok; ++j, c += 2) {
+            const uint32_t f = c % FS, slot = c % KS;
+            bool here = wait(sf_full + 8 * f, (c / FS) & 1, 510);
             if (here && c >= KS) here = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 520);
             ok = __all_sync(0xffffffffu, here);
             if (!ok) break;
@@ -537,16 +586,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
             for (int i = 0; i < ns; ++i) {
               const uint4 v = *reinterpret_cast<const uint4*>(src + i * (TILE * 128) + rr * 128 + ((u ^ sw) << 4));
               uint4 o0, o1;
-              auto cvt = [](uint32_t x, uint32_t& lo, uint32_t& hi) {
-                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-                    "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-                    : "=r"(lo), "=r"(hi)
-                    : "r"(x));
-              };
-              cvt(v.x, o0.x, o0.y);
-              cvt(v.y, o0.z, o0.w);
-              cvt(v.z, o1.x, o1.y);
-              cvt(v.w, o1.z, o1.w);
+              f16_of_e4m3(v.x, o0.x, o0.y);
+              f16_of_e4m3(v.y, o0.z, o0.w);
+              f16_of_e4m3(v.z, o1.x, o1.y);
+              f16_of_e4m3(v.w, o1.z, o1.w);
               if (zero && w.hidden(w.slab(j * WP_SLABS + i) * TILE + rr)) o0 = o1 = make_uint4(0, 0, 0, 0);
               uint8_t* p = kv == 0 ? dst + cc * (WP_KEYS * 128) + (i * TILE + rr) * 128
                                    : dst + i * (2 * TILE * 128) + cc * (TILE * 128) + rr * 128;
@@ -570,10 +613,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     const uint32_t o_addr = lane_addr + 256 + 128 * X;
     const float sl = a.scale_log2;
     uint32_t n_s = 0, no = 0;  // S tiles and outputs taken
-    for (int64_t idx = begin; idx < n_items && ok; idx += step) {
-      if (!get(idx, w, X == 0 && tid == 0 && rank == 0)) continue;
+    while (ok && next_item(w)) {
       if (X >= w.nq) continue;
-      const int qi = w.i0 + X * QB + r / G, h = r % G;
+      const int qi = w.i0 + X * QB + r / G;
       const bool valid = r < QB * G && qi < w.i1;
       const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
@@ -675,21 +717,43 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       }
       if (csize == 1) {
         const float inv = a.v_mul / l;  // v_scale of an E4M3 pool, else 1
-        T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(w.qbeg + qi) * a.H_q + w.g * G + h) * D;
+        // the 16-byte pieces of four rows change places within a quad of lanes, so that a store covers 64 bytes
+        // in a row of eight rows, not 16 of 32: piece p of 32 columns of the quad's row i in lane p
+        T* out[4];
+        const int r4 = r & ~3, q4 = lane & 3;
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int qr = w.i0 + X * QB + (r4 + i) / G, hr = (r4 + i) % G;
+          const bool there = r4 + i < QB * G && qr < w.i1;
+          out[i] = there ? static_cast<T*>(a.out) + (static_cast<int64_t>(w.qbeg + qr) * a.H_q + w.g * G + hr) * D + 8 * q4
+                         : nullptr;
+        }
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
+          uint32_t o[32], v[4][4];
           tmem_ld32(o_addr + 32 * c, o);
           tmem_ld_wait();
-          if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dst[v] = make_uint4(pack2<T>(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
-                                  pack2<T>(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
-                                  pack2<T>(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
-                                  pack2<T>(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
-          }
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[p][e] = pack2<T>(__uint_as_float(o[8 * p + 2 * e]) * inv, __uint_as_float(o[8 * p + 2 * e + 1]) * inv);
+#pragma unroll
+          for (int bit = 1; bit < 4; bit *= 2)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              if (p & bit) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const bool up = q4 & bit;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[p][e] : v[p | bit][e], bit);
+                v[p][e] = up ? got : v[p][e];
+                v[p | bit][e] = up ? v[p | bit][e] : got;
+              }
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (out[i]) *reinterpret_cast<uint4*>(out[i] + 32 * c) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
         }
         tc_fence_before();
       } else {
@@ -719,8 +783,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   if (warp == 8) tmem_dealloc(tmem, 512);
   if (csize > 1) {
     // every thread of the cluster; an item is the same for all its CTAs, and so is its absence
-    Item it;
-    const bool has = begin < n_items && get(begin, it, false);
+    const Item it = items_p[0];
+    const bool has = it.work != 0;
     cluster_barrier();
     if (has && !*abort_flag) {
       constexpr int PC = D / 4;  // 16-byte pieces of a row's O
