@@ -404,12 +404,19 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // divergent thread on its own needs some 140 cycles a product to bring its operands into uniform registers.
       // S has two buffers, so that Q K of the next key tile runs while this one's softmax does, and a softmax finds its
       // scores ready.  A tile without rows (nq = 1) takes its part in the operand ring all the same.
-      const int X = warp == 9 ? 0 : 1;
-      const uint32_t s_tm = tmem + 128 * X, o_tm = tmem + 256 + 128 * X;
+      // (the broadcasts from lane 0 are what tells the compiler that a value is the same in all lanes)
+      auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+      const int X = uni(warp == 9 ? 0 : 1);
+      const uint32_t s_tm = uni(tmem) + 128 * X, o_tm = uni(tmem) + 256 + 128 * X;
       const uint32_t idesc_o = umma_idesc_f16(BF16, 128, D, true);
       // operand descriptors: the first, and a step of the address field (16-byte units) from there on
-      const uint64_t q_desc = umma_desc_sw128(qs + X * C::Q_TILE, 16, 1024), k_desc = umma_desc_sw128(ring, 16, 1024);
-      const uint64_t v_desc = umma_desc_sw128(ring, TILE * 128, 1024);
+      const uint64_t q_desc = umma_desc_sw128(uni(qs) + X * C::Q_TILE, 16, 1024);
+      const uint64_t k_desc = umma_desc_sw128(uni(ring), 16, 1024);
+      const uint64_t v_desc = umma_desc_sw128(uni(ring), TILE * 128, 1024);
+      const uint32_t bars = uni(q_full);  // the barriers from here on
+      const uint32_t u_empty = bars + (empty - q_full), u_q_empty = bars + 16;
+      const uint32_t u_s_full = bars + (s_full - q_full) + 16 * X, u_o_done = bars + (o_done - q_full) + 8 * X;
+      const uint32_t u_o_full = bars + (o_full - q_full) + 8 * X;
       auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
         return __all_sync(0xffffffffu, wait(bar, parity, where)) != 0;
       };
@@ -419,8 +426,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       uint32_t c = 0, items = 0, ns_ = 0, np = 0;  // ring position of the item's first K; items; S and P tiles so far
       while (ok && next_item(w)) {
         if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
-        const bool live = X < w.nq;
-        const int nt = w.j1 - w.j0;
+        const bool live = uni(X < w.nq) != 0;
+        const int nt = uni(w.j1 - w.j0), nslab = uni(w.nslab - w.j0 * WP_SLABS);
         ok = wait_all(KV8 ? q_ready : q_full, items++ & 1, 200);
         // S of the item's i-th key tile (its K is at ring position c + 2 i)
         auto qk = [&](int i) -> bool {
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (!wait_all(full + 8 * slot, (at / KS) & 1, 210)) return false;
           tc_fence_after();
           const uint64_t kd = k_desc + slot * (C::KV_TILE / 16);
-          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, w.slabs_of(w.j0 + i) * TILE, false);
+          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, min(WP_SLABS, nslab - i * WP_SLABS) * TILE, false);
           const uint32_t b = ns_ & 1;
           if (elect_one()) {
             if (live) {
@@ -436,9 +443,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               for (int k = 0; k < D / 16; ++k)  // 64-wide chunk; 16 elements along its 128-byte row
                 umma_ss(s_tm + 64 * b, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
                         kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
-              umma_commit(s_full + 16 * X + 8 * b);
-              umma_commit(empty + 8 * slot);  // this tile's use of the operand is over once its products are done
-              if (i + 1 == nt) umma_commit(q_empty);
+              umma_commit(u_s_full + 8 * b);
+              umma_commit(u_empty + 8 * slot);  // this tile's use of the operand is over once its products are done
+              if (i + 1 == nt) umma_commit(u_q_empty);
             } else {
               mbar_arrive(empty + 8 * slot);
               if (i + 1 == nt) mbar_arrive(q_empty);
@@ -454,16 +461,16 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (live && !wait_all(p_full + 16 * X + 8 * b, (np >> 1) & 1, 230)) return false;
           tc_fence_after();
           const uint64_t vd = v_desc + slot * (C::KV_TILE / 16);
-          const int n = w.slabs_of(w.j0 + i);
+          const int n = min(WP_SLABS, nslab - i * WP_SLABS);
           if (elect_one()) {
             if (live) {
 #pragma unroll
               for (int k = 0; k < WP_SLABS; ++k)
                 if (k < n)
                   umma_ts(o_tm, s_tm + 64 * b + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
-              umma_commit(o_done + 8 * X);
-              if (i + 1 == nt) umma_commit(o_full + 8 * X);
-              umma_commit(empty + 8 * slot);
+              umma_commit(u_o_done);
+              if (i + 1 == nt) umma_commit(u_o_full);
+              umma_commit(u_empty + 8 * slot);
             } else {
               mbar_arrive(empty + 8 * slot);
             }
