@@ -41,7 +41,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int WP_KEYS = 64, WP_SLABS = WP_KEYS / TILE;
+constexpr int WP_KEYS = 128, WP_SLABS = WP_KEYS / TILE;
 constexpr int WP_TBL = 256;  // entries of the table that finds an item's sequence
 
 template <bool KV8, int D>
@@ -51,9 +51,9 @@ struct WpCfg {
   static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
   static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile as an operand (16-bit)
   static constexpr int STG_TILE = WP_KEYS * D;            // one K or V tile of E4M3 codes
-  static constexpr int KS = KV8 ? 6 : (D == 64 ? 16 : 10);  // operand ring: K and V tiles in turn
-  static constexpr int FS = KV8 ? 8 : 0;                  // staging ring
-  static constexpr int BARS = 3 + 3 * KS + 4 + 4 + 3 * 2 + 4 + 2 * FS;
+  static constexpr int KS = KV8 ? 3 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
+  static constexpr int FS = KV8 ? 4 : 0;                  // staging ring
+  static constexpr int BARS = 3 + 3 * KS + 6 * 2 + 4 + 2 * FS;
   static constexpr int READERS = THREADS / 32 - 1;        // warps that follow the items
   static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
   static constexpr int SMEM = 1024 + DATA + (BARS + 1) * 8 + 16 + 2 * 64 + 96 + (WP_TBL + 1) * 4;
@@ -171,9 +171,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   uint8_t* bar_p = base + C::DATA;
   const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
-  // per tile A, B: S of an even, odd key tile; P likewise; P V done; the item's O done; after an abort
-  const uint32_t s_full = land + 8 * KS, p_full = s_full + 32, o_done = p_full + 32, o_full = o_done + 16;
-  const uint32_t drain = o_full + 16, sf_full = drain + 16, sf_empty = sf_full + 8 * FS;  // staging ring
+  // per tile A, B: S; the first three quarters of P, all of it; the item's O; the turn to issue; after an abort
+  const uint32_t s_full = land + 8 * KS, p_most = s_full + 16, p_full = p_most + 16, o_full = p_full + 16;
+  const uint32_t turn = o_full + 16, drain = turn + 16;
+  const uint32_t sf_full = drain + 16, sf_empty = sf_full + 8 * FS;  // staging ring
   const uint32_t it_full = sf_full + 16 * FS, it_empty = it_full + 16;  // items, two places
   uint8_t* tail_p = bar_p + (C::BARS + 1) / 2 * 16;
   Item* items_p = reinterpret_cast<Item*>(tail_p);
@@ -192,11 +193,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       mbar_init(land + 8 * k, 1);
     }
     for (int x = 0; x < 2; ++x) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(s_full + 16 * x + 8 * b, 1);
-        mbar_init(p_full + 16 * x + 8 * b, 4);
-      }
-      mbar_init(o_done + 8 * x, 1);
+      mbar_init(s_full + 8 * x, 1);
+      mbar_init(p_most + 8 * x, 4);  // one arrival a warp
+      mbar_init(p_full + 8 * x, 4);
+      mbar_init(turn + 8 * x, 1);
       mbar_init(o_full + 8 * x, 1);
       mbar_init(drain + 8 * x, 1);
     }
@@ -402,8 +402,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // ------------------------------------------------------------ the products of tile X (9: A, 11: B)
       // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
       // divergent thread on its own needs some 140 cycles a product to bring its operands into uniform registers.
-      // S has two buffers, so that Q K of the next key tile runs while this one's softmax does, and a softmax finds its
-      // scores ready.  A tile without rows (nq = 1) takes its part in the operand ring all the same.
+      // A and B take turns, (P V, Q K) of one, then of the other, so that S of A arrives while B's products run and the
+      // two softmaxes stay half a period apart; issued side by side, the products of both end together, and then both
+      // softmaxes run while the tensor cores wait.  A tile without rows (nq = 1) has its turns all the same.
       // (the broadcasts from lane 0 are what tells the compiler that a value is the same in all lanes)
       auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
       const int X = uni(warp == 9 ? 0 : 1);
@@ -415,77 +416,85 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       const uint64_t v_desc = umma_desc_sw128(uni(ring), TILE * 128, 1024);
       const uint32_t bars = uni(q_full);  // the barriers from here on
       const uint32_t u_empty = bars + (empty - q_full), u_q_empty = bars + 16;
-      const uint32_t u_s_full = bars + (s_full - q_full) + 16 * X, u_o_done = bars + (o_done - q_full) + 8 * X;
-      const uint32_t u_o_full = bars + (o_full - q_full) + 8 * X;
+      const uint32_t u_s_full = bars + (s_full - q_full) + 8 * X, u_o_full = bars + (o_full - q_full) + 8 * X;
+      const uint32_t u_turn = bars + (turn - q_full) + 8 * (1 - X);  // the other tile's
       auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
         return __all_sync(0xffffffffu, wait(bar, parity, where)) != 0;
       };
       auto commit = [&](uint32_t bar) {
         if (elect_one()) umma_commit(bar);
       };
-      uint32_t c = 0, items = 0, ns_ = 0, np = 0;  // ring position of the item's first K; items; S and P tiles so far
+      uint32_t c = 0, items = 0, np = 0, turns = 0;  // ring position; items; P tiles taken; turns had
       while (ok && next_item(w)) {
         if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
         const bool live = uni(X < w.nq) != 0;
         const int nt = uni(w.j1 - w.j0), nslab = uni(w.nslab - w.j0 * WP_SLABS);
         ok = wait_all(KV8 ? q_ready : q_full, items++ & 1, 200);
-        // S of the item's i-th key tile (its K is at ring position c + 2 i)
-        auto qk = [&](int i) -> bool {
-          const uint32_t at = c + 2 * i, slot = at % KS;
-          if (!wait_all(full + 8 * slot, (at / KS) & 1, 210)) return false;
+        for (int i = -1; i < nt && ok; ++i) {  // P V of the item's i-th key tile, then Q K of the next
+          // everything is waited for before the turn: within it the products follow each other without a gap
+          const bool has_pv = i >= 0, has_qk = i + 1 < nt;
+          const uint32_t vs = c % KS, ks = (c + has_pv) % KS;
+          if (has_pv) {
+            ok = wait_all(full + 8 * vs, (c / KS) & 1, 210);
+            ++c;
+          }
+          if (ok && has_qk) {
+            ok = wait_all(full + 8 * ks, (c / KS) & 1, 220);
+            ++c;
+          }
+          if (ok && has_pv && live) ok = wait_all(p_most + 8 * X, np & 1, 230);
+          if (ok && (X == 1 || turns > 0)) ok = wait_all(turn + 8 * X, (turns - 1 + X) & 1, 240);
+          if (!ok) break;
+          ++turns;
           tc_fence_after();
-          const uint64_t kd = k_desc + slot * (C::KV_TILE / 16);
-          const uint32_t idesc_s = umma_idesc_f16(BF16, 128, min(WP_SLABS, nslab - i * WP_SLABS) * TILE, false);
-          const uint32_t b = ns_ & 1;
+          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * (C::KV_TILE / 16);
+          const int nv = has_pv ? min(WP_SLABS, nslab - i * WP_SLABS) : 0;
+          const uint32_t idesc_s =
+              umma_idesc_f16(BF16, 128, has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE, false);
+          auto pv = [&](int k) {
+            if (k < nv)
+              umma_ts(o_tm, s_tm + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+          };
+          if (live && has_pv) {  // three quarters of P, then (it came meanwhile) the rest
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < WP_SLABS * 3 / 4; ++k) pv(k);
+            }
+            __syncwarp();
+            ok = wait_all(p_full + 8 * X, np++ & 1, 250);
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (elect_one()) {
             if (live) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k)  // 64-wide chunk; 16 elements along its 128-byte row
-                umma_ss(s_tm + 64 * b, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
-                        kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
-              umma_commit(u_s_full + 8 * b);
-              umma_commit(u_empty + 8 * slot);  // this tile's use of the operand is over once its products are done
-              if (i + 1 == nt) umma_commit(u_q_empty);
-            } else {
-              mbar_arrive(empty + 8 * slot);
-              if (i + 1 == nt) mbar_arrive(q_empty);
-            }
-          }
-          __syncwarp();
-          ++ns_;
-          return true;
-        };
-        auto pv = [&](int i) -> bool {
-          const uint32_t at = c + 2 * i + 1, slot = at % KS, b = np & 1;
-          if (!wait_all(full + 8 * slot, (at / KS) & 1, 220)) return false;
-          if (live && !wait_all(p_full + 16 * X + 8 * b, (np >> 1) & 1, 230)) return false;
-          tc_fence_after();
-          const uint64_t vd = v_desc + slot * (C::KV_TILE / 16);
-          const int n = min(WP_SLABS, nslab - i * WP_SLABS);
-          if (elect_one()) {
-            if (live) {
+              for (int k = WP_SLABS * 3 / 4; k < WP_SLABS; ++k) pv(k);
+              if (has_qk) {
 #pragma unroll
-              for (int k = 0; k < WP_SLABS; ++k)
-                if (k < n)
-                  umma_ts(o_tm, s_tm + 64 * b + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
-              umma_commit(u_o_done);
-              if (i + 1 == nt) umma_commit(u_o_full);
-              umma_commit(u_empty + 8 * slot);
+                for (int k = 0; k < D / 16; ++k) {  // 64-wide chunk; 16 elements along its 128-byte row
+                  // the other tile's warp is let go two products early, which hides its start
+                  if (k == D / 16 - 2) mbar_arrive(u_turn);
+                  umma_ss(s_tm, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
+                          kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
+                }
+                umma_commit(u_s_full);
+              } else {
+                mbar_arrive(u_turn);
+                umma_commit(u_o_full);
+              }
+              // this tile's use of the operands is over once its products so far are done
+              if (has_pv) umma_commit(u_empty + 8 * vs);
+              if (has_qk) umma_commit(u_empty + 8 * ks);
+              if (i + 2 == nt) umma_commit(u_q_empty);
             } else {
-              mbar_arrive(empty + 8 * slot);
+              mbar_arrive(u_turn);
+              if (has_pv) mbar_arrive(u_empty + 8 * vs);
+              if (has_qk) mbar_arrive(u_empty + 8 * ks);
+              if (i + 2 == nt) mbar_arrive(u_q_empty);
             }
           }
           __syncwarp();
-          ++np;
-          return true;
-        };
-        if (ok) ok = qk(0);
-        for (int i = 0; i < nt && ok; ++i) {
-          if (i + 1 < nt) ok = qk(i + 1);
-          if (ok) ok = pv(i);
         }
-        c += 2 * nt;
-        if (!live) ns_ -= nt, np -= nt;  // no S or P of this tile
       }
       if (*abort_flag) {
         commit(drain + 8 * X);
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::R_SOFTMAX));
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t o_addr = lane_addr + 256 + 128 * X;
+    const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
     const float sl = a.scale_log2;
     uint32_t n_s = 0, no = 0;  // S tiles and outputs taken
     while (ok && next_item(w)) {
@@ -628,11 +637,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
       float m = -INFINITY, l = 0.f;
       for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
-        const uint32_t b = n_s & 1, s_addr = lane_addr + 128 * X + 64 * b;
-        ok = __all_sync(0xffffffffu, wait(s_full + 16 * X + 8 * b, (n_s >> 1) & 1, 600));
+        ok = __all_sync(0xffffffffu, wait(s_full + 8 * X, n_s & 1, 600));
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[2][32];
+        uint32_t sv[4][32];
         tmem_ld32(s_addr, sv[0]);
         tmem_ld32(s_addr + 32, sv[1]);
         // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
@@ -640,40 +648,43 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
         const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
         tmem_ld_wait();
-        if (edge) {
+        tmem_ld32(s_addr + 64, sv[2]);  // on their way during the first half's maximum
+        tmem_ld32(s_addr + 96, sv[3]);
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < WP_SLABS; ++i) {
-            // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
-            // window (selects, no branches: 64 short branches cost ten times the softmax itself)
-            const int t0 = w.slab(u0 + i) * TILE;
-            const uint32_t vis = i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
-            if (__any_sync(0xffffffffu, vis != 0xffffu)) {
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) tmem_ld_wait();
+          if (edge) {
 #pragma unroll
-              for (int e = 0; e < TILE; ++e) {
-                uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
-                x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
+            for (int i = 4 * h; i < 4 * h + 4; ++i) {
+              // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
+              // window (selects, no branches: 128 short branches cost ten times the softmax itself)
+              const int t0 = w.slab(u0 + i) * TILE;
+              const uint32_t vis = i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+              if (__any_sync(0xffffffffu, vis != 0xffffu)) {
+#pragma unroll
+                for (int e = 0; e < TILE; ++e) {
+                  uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
+                  x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
+                }
               }
             }
           }
+#pragma unroll
+          for (int c = 2 * h; c < 2 * h + 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(sv[c][e + t]), __uint_as_float(sv[c][e + t + 4])));
         }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(sv[c][e + t]), __uint_as_float(sv[c][e + t + 4])));
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const float m_new = fmaxf(m, mx * sl);
         // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
-        // l and O so far are rescaled, once O holds P V(j - 1)
+        // l and O so far are rescaled; S(j) is here, so O holds P V(j - 1)
         if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
           const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
           if (j > w.j0) {
-            ok = __all_sync(0xffffffffu, wait(o_done + 8 * X, (n_s - 1) & 1, 610));
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -694,7 +705,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
 #pragma unroll
         for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -705,13 +716,15 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
             pw[e] = pack2<TP>(p.x, p.y);
           }
           tmem_st16(s_addr + 16 * c, pw);
+          if (c >= 2) {  // P V may begin with three quarters of the keys
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive((c == 2 ? p_most : p_full) + 8 * X);
+          }
         }
         const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
         l += l2.x + l2.y;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 16 * X + 8 * b);
       }
       if (!ok) break;
       if (w.j0 < w.j1) {
