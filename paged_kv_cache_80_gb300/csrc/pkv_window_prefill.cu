@@ -18,7 +18,7 @@
 // Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 and 11
 // issue the products of A and of B; 10 loads Q and zeroes V rows that no row sees (0 times whatever lies there must
 // stay 0).  E4M3 pools: 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16.
-// TMEM: S of A and B (128 columns each; P overwrites its first 64), O of A and B from column 256 on.
+// TMEM: S of A and B (128 columns each; P overwrites its last 64), O of A and B from column 256 on.
 // A tile's products are issued by one thread and taken in order, ..., P V(j), Q K(j + 1), ...: S(j + 1) may go over
 // P(j), and its arrival says that O holds P V(j).
 //
@@ -451,14 +451,16 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           const int nv = has_pv ? min(WP_SLABS, nslab - i * WP_SLABS) : 0;
           const uint32_t idesc_s =
               umma_idesc_f16(BF16, 128, has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE, false);
+          // P of keys 0 .. 31 and 64 .. 127 comes first (slabs 0, 1, 4 .. 7; slab 0 is always there)
           auto pv = [&](int k) {
             if (k < nv)
-              umma_ts(o_tm, s_tm + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+              umma_ts(o_tm, s_tm + 64 + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
           };
           if (live && has_pv) {  // three quarters of P, then (it came meanwhile) the rest
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < WP_SLABS * 3 / 4; ++k) pv(k);
+              for (int k = 0; k < WP_SLABS; ++k)
+                if (k < 2 || k >= 4) pv(k);
             }
             __syncwarp();
             ok = wait_all(p_full + 8 * X, np++ & 1, 250);
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (elect_one()) {
             if (live) {
 #pragma unroll
-              for (int k = WP_SLABS * 3 / 4; k < WP_SLABS; ++k) pv(k);
+              for (int k = 2; k < 4; ++k) pv(k);
               if (has_qk) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {  // 64-wide chunk; 16 elements along its 128-byte row
@@ -640,44 +642,47 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         ok = __all_sync(0xffffffffu, wait(s_full + 8 * X, n_s & 1, 600));
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[4][32];
-        tmem_ld32(s_addr, sv[0]);
-        tmem_ld32(s_addr + 32, sv[1]);
+        uint32_t sa[2][32], sb[2][32];  // the first 64 keys and the others
+        tmem_ld32(s_addr, sa[0]);
+        tmem_ld32(s_addr + 32, sa[1]);
         // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
         const int u0 = j * WP_SLABS, n = w.slabs_of(j);
         const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
         const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
-        tmem_ld_wait();
-        tmem_ld32(s_addr + 64, sv[2]);  // on their way during the first half's maximum
-        tmem_ld32(s_addr + 96, sv[3]);
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto mask = [&](uint32_t (&x)[2][32], int i0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) tmem_ld_wait();
-          if (edge) {
+          for (int i = 0; i < 4; ++i) {
+            // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
+            // window (selects, no branches: 128 short branches cost ten times the softmax itself)
+            const int t0 = w.slab(u0 + i0 + i) * TILE;
+            const uint32_t vis = i0 + i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+            if (__any_sync(0xffffffffu, vis != 0xffffu)) {
 #pragma unroll
-            for (int i = 4 * h; i < 4 * h + 4; ++i) {
-              // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
-              // window (selects, no branches: 128 short branches cost ten times the softmax itself)
-              const int t0 = w.slab(u0 + i) * TILE;
-              const uint32_t vis = i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
-              if (__any_sync(0xffffffffu, vis != 0xffffu)) {
-#pragma unroll
-                for (int e = 0; e < TILE; ++e) {
-                  uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
-                  x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
-                }
+              for (int e = 0; e < TILE; ++e) {
+                uint32_t& v = x[i >> 1][(i & 1) * TILE + e];
+                v = (vis & (1u << e)) ? v : __float_as_uint(-INFINITY);
               }
             }
           }
+        };
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&](const uint32_t (&x)[2][32]) {
 #pragma unroll
-          for (int c = 2 * h; c < 2 * h + 2; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
 #pragma unroll
               for (int t = 0; t < 4; ++t)
-                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(sv[c][e + t]), __uint_as_float(sv[c][e + t + 4])));
-        }
+                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(x[c][e + t]), __uint_as_float(x[c][e + t + 4])));
+        };
+        tmem_ld_wait();
+        tmem_ld32(s_addr + 64, sb[0]);  // on their way during the first half's maximum
+        tmem_ld32(s_addr + 96, sb[1]);
+        if (edge) mask(sa, 0);
+        largest(sa);
+        tmem_ld_wait();
+        if (edge) mask(sb, 4);
+        largest(sb);
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const float m_new = fmaxf(m, mx * sl);
         // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
@@ -698,31 +703,43 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           l *= alpha;
           m = m_new;
         }
-        // P = 2^(scale s - m), 16-bit, two keys a column, over the S just read; a row that has seen no key yet
-        // keeps m = -inf, and 0 stands in for it
+        // P = 2^(scale s - m), 16-bit, two keys a column, over S of the other keys, which are taken first: E4M3 pools,
+        // whose softmax has fewer registers, read S of the first 64 a second time instead of keeping it; a row that
+        // has seen no key yet keeps m = -inf, and 0 stands in for it
         const float neg_m = m == -INFINITY ? 0.f : -m;
         float2 ls[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        auto exps = [&](const uint32_t (&x)[32], uint32_t at) {
           uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 p = fma2(make_float2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])),
-                            make_float2(sl, sl), make_float2(neg_m, neg_m));
+            float2 p = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(sl, sl),
+                            make_float2(neg_m, neg_m));
             p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
             ls[e & 3] = add2(ls[e & 3], p);
             pw[e] = pack2<TP>(p.x, p.y);
           }
-          tmem_st16(s_addr + 16 * c, pw);
-          if (c >= 2) {  // P V may begin with three quarters of the keys
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive((c == 2 ? p_most : p_full) + 8 * X);
-          }
+          tmem_st16(at, pw);
+        };
+        auto arrive = [&](uint32_t bar) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+        exps(sb[0], s_addr + 96);
+        exps(sb[1], s_addr + 112);
+        if constexpr (KV8) {
+          tmem_ld32(s_addr, sa[0]);
+          tmem_ld32(s_addr + 32, sa[1]);
+          tmem_ld_wait();
+          if (edge) mask(sa, 0);
         }
+        exps(sa[0], s_addr + 64);
+        arrive(p_most + 8 * X);  // P V may begin with three quarters of the keys
+        exps(sa[1], s_addr + 80);
+        arrive(p_full + 8 * X);
         const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
         l += l2.x + l2.y;
       }
