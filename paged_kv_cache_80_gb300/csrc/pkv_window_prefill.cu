@@ -17,7 +17,8 @@
 //
 // Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 and 11
 // issue the products of A and of B; 10 loads Q and zeroes V rows that no row sees (0 times whatever lies there must
-// stay 0).  E4M3 pools: 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16.
+// stay 0).  E4M3 pools: K codes are an operand as they are, with q as the sum of two E4M3 numbers (two products at
+// twice the rate), and V codes are converted to binary16, both by warps 12-15.
 // TMEM: S of A and B (128 columns each; P overwrites its last 64), O of A and B from column 256 on.
 // A tile's products are issued by one thread and taken in order, ..., P V(j), Q K(j + 1), ...: S(j + 1) may go over
 // P(j), and its arrival says that O holds P V(j).
@@ -42,25 +43,26 @@ namespace pkv {
 namespace {
 
 constexpr int WP_KEYS = 128, WP_SLABS = WP_KEYS / TILE;
-constexpr int WP_TBL = 256;  // entries of the table that finds an item's sequence
 
 template <bool KV8, int D>
 struct WpCfg {
-  static constexpr int THREADS = KV8 ? 640 : 384;
+  static constexpr int THREADS = KV8 ? 512 : 384;
+  static constexpr int TBL = KV8 ? 128 : 256;             // entries of the table that finds an item's sequence
   static constexpr int NCH = D / 64;                      // 64-wide chunks of d (128 bytes, the swizzle's width)
-  static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
-  static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile as an operand (16-bit)
-  static constexpr int STG_TILE = WP_KEYS * D;            // one K or V tile of E4M3 codes
-  static constexpr int KS = KV8 ? 3 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
-  static constexpr int FS = KV8 ? 4 : 0;                  // staging ring
-  static constexpr int BARS = 3 + 3 * KS + 6 * 2 + 4 + 2 * FS;
+  static constexpr int Q_TILE = 128 * D * 2;              // one Q tile (E4M3: its two parts, below)
+  static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile of 16-bit operands
+  static constexpr int F8_TILE = WP_KEYS * D;             // one of E4M3 codes
+  // 16-bit pools: one ring of KS operands, K and V tiles in turn.  E4M3 pools: KS K tiles, FS staged V tiles and VS
+  // converted ones.
+  static constexpr int KS = KV8 ? 4 : (D == 64 ? 8 : 5), FS = KV8 ? 2 : 0, VS = KV8 ? 2 : 0;
+  static constexpr int DATA = 2 * Q_TILE + (KV8 ? KS * F8_TILE + VS * KV_TILE + FS * F8_TILE : KS * KV_TILE);
+  static constexpr int BARS = 3 + 3 * KS + 6 * 2 + 4 + 2 * FS + 2 * VS;
   static constexpr int READERS = THREADS / 32 - 1;        // warps that follow the items
-  static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
-  static constexpr int SMEM = 1024 + DATA + (BARS + 1) * 8 + 16 + 2 * 64 + 96 + (WP_TBL + 1) * 4;
+  static constexpr int SMEM = 1024 + DATA + (BARS + 1) * 8 + 16 + 2 * 64 + 96 + (TBL + 1) * 4 + (KV8 ? 512 : 0);
   // registers: the launch's share is 65,536 / THREADS rounded down to a multiple of 8
-  static constexpr int R_LAUNCH = KV8 ? 96 : 168;
-  static constexpr int R_SOFTMAX = KV8 ? 160 : 208, R_CONTROL = KV8 ? 64 : 88, R_CONVERT = 48;
-  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 256 * R_CONVERT : 0) <= THREADS * R_LAUNCH, "register split");
+  static constexpr int R_LAUNCH = KV8 ? 128 : 168;
+  static constexpr int R_SOFTMAX = KV8 ? 168 : 208, R_CONTROL = KV8 ? 72 : 88, R_CONVERT = 96;
+  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 128 * R_CONVERT : 0) <= THREADS * R_LAUNCH, "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -104,16 +106,32 @@ __device__ __forceinline__ uint32_t below(int n) {
   return (1u << k) - 1u;
 }
 
-// four E4M3 codes to binary16 (exact), and two bfloat16 rounded to binary16, the first of each pair low
+// four E4M3 codes to binary16 (exact), the first of each pair low
 __device__ __forceinline__ void f16_of_e4m3(uint32_t x, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
 }
-__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t x) {
-  const __half2 h = __floats2half2_rn(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-  return *reinterpret_cast<const uint32_t*>(&h);
+// two values to E4M3 codes (the first low), and the rest that the codes leave of them, as codes
+__device__ __forceinline__ void e4m3_split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+  uint32_t h2;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(h2) : "r"(hi));
+  const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+  lo = __nv_cvt_float2_to_fp8x2(make_float2(x - back.x, y - back.y), __NV_SATFINITE, __NV_E4M3);
+}
+
+// D(tmem) (+)= A(smem) B(smem)^T on 8-bit operands, K = 32
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: binary32 accumulator, A and B both E4M3 (format 0) and K-major
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 __device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
@@ -156,9 +174,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmv, const DecodeArgs a, const int32_t* __restrict__ q_off,
                        int32_t max_q, int32_t csize, int64_t most_items) {
   using C = WpCfg<KV8, D>;
-  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // operand type of the products
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // type of P and V as operands
   using TP = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr int KS = C::KS, FS = C::FS;
+  constexpr int KS = C::KS, FS = C::FS, VS = C::VS;
   extern __shared__ uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.G, QB = 128 / G;  // queries a tile
@@ -167,28 +185,31 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t qs = smem_u32(base), ring = qs + 2 * C::Q_TILE;
   uint8_t* ring_p = base + 2 * C::Q_TILE;
-  uint8_t* stg_p = ring_p + KS * C::KV_TILE;
+  uint8_t* vop_p = ring_p + KS * C::F8_TILE;  // E4M3: converted V tiles, then staged ones
+  uint8_t* stg_p = vop_p + VS * C::KV_TILE;
   uint8_t* bar_p = base + C::DATA;
   const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
   // per tile A, B: S; the first three quarters of P, all of it; the item's O; the turn to issue; after an abort
   const uint32_t s_full = land + 8 * KS, p_most = s_full + 16, p_full = p_most + 16, o_full = p_full + 16;
   const uint32_t turn = o_full + 16, drain = turn + 16;
-  const uint32_t sf_full = drain + 16, sf_empty = sf_full + 8 * FS;  // staging ring
-  const uint32_t it_full = sf_full + 16 * FS, it_empty = it_full + 16;  // items, two places
+  const uint32_t sf_full = drain + 16, sf_empty = sf_full + 8 * FS;             // staged V (E4M3)
+  const uint32_t vo_full = sf_empty + 8 * FS, vo_empty = vo_full + 8 * VS;      // converted V
+  const uint32_t it_full = vo_empty + 8 * VS, it_empty = it_full + 16;          // items, two places
   uint8_t* tail_p = bar_p + (C::BARS + 1) / 2 * 16;
   Item* items_p = reinterpret_cast<Item*>(tail_p);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(tail_p + 2 * sizeof(Item));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int32_t* wsum = reinterpret_cast<int32_t*>(tslot + 4);
-  int32_t* pre = wsum + 24;  // [groups + 1]: query-block pairs of the sequences before a group of them
+  int8_t* q_exp = reinterpret_cast<int8_t*>(wsum + 24);  // E4M3: exponents of the rows' q, of two items in turn
+  int32_t* pre = wsum + 24 + (KV8 ? 128 : 0);  // [groups + 1]: query-block pairs of the sequences before a group of them
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_ready, 8);  // one arrival a warp
+    mbar_init(q_ready, 4);  // one arrival a warp
     mbar_init(q_empty, 2);
     for (int k = 0; k < KS; ++k) {
-      mbar_init(full + 8 * k, KV8 ? 4 : 1);
+      mbar_init(full + 8 * k, 1);
       mbar_init(empty + 8 * k, 2);  // both tiles' products
       mbar_init(land + 8 * k, 1);
     }
@@ -204,6 +225,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       mbar_init(sf_full + 8 * k, 1);
       mbar_init(sf_empty + 8 * k, 4);
     }
+    for (int k = 0; k < VS; ++k) {
+      mbar_init(vo_full + 8 * k, 4);
+      mbar_init(vo_empty + 8 * k, 2);
+    }
     for (int k = 0; k < 2; ++k) {
       mbar_init(it_full + 8 * k, 1);
       mbar_init(it_empty + 8 * k, C::READERS);
@@ -214,9 +239,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   if (warp == 8) tmem_alloc(smem_u32(tslot), 512);
 
   // ---- the items, counted ahead so that ragged chunks leave no holes: a thread counts the query-block pairs of
-  // `per` sequences (one, up to WP_TBL of them), and the table holds the sums before each such group
+  // `per` sequences (one, up to C::TBL of them), and the table holds the sums before each such group
   const int most = (max_q + 2 * QB - 1) / (2 * QB);  // query-block pairs of a chunk at most
-  const int per = (a.n_seq + WP_TBL - 1) / WP_TBL, groups = (a.n_seq + per - 1) / per;
+  const int per = (a.n_seq + C::TBL - 1) / C::TBL, groups = (a.n_seq + per - 1) / per;
   auto pairs_of = [&](int s, bool record) -> int {
     const int q0 = q_off[s], c = q_off[s + 1] - q0;
     if (q0 < 0 || c < 0 || c > a.n_tok - q0) {
@@ -335,11 +360,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // Lane i holds the pool row of slab 32 k + i of the list (the next 32 are looked up ahead); the 8 lanes of tile
       // j copy its slabs.  16-bit pools: a K slab as one box per 64-wide chunk ([chunk][128 keys][128 B]), a V slab
       // as one box of all chunks ([slab][chunk][16 keys][128 B]); E4M3 pools: 2 KB of codes into the staging ring.
-      constexpr int RS = KV8 ? FS : KS;
-      const uint32_t r_full = KV8 ? sf_full : full, r_empty = KV8 ? sf_empty : empty;
-      const uint32_t r_data = KV8 ? smem_u32(stg_p) : ring;
-      uint32_t c = 0;  // tiles loaded so far
-      uint32_t on_land = 0;  // of the last RS tiles, those whose bytes arrive at `land` (bit c % RS)
+      uint32_t c = 0;  // tiles loaded so far (E4M3: pairs of them)
+      uint32_t on_land = 0;  // of the last KS tiles, those whose bytes arrive at `land` (bit c % KS)
       uint32_t land_par = 0;  // bit k: parity of the uses of `land` slot k
       while (ok && next_item(w)) {
         auto row_of = [&](int u) -> int {
@@ -363,41 +385,64 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           }
           const int ns = w.slabs_of(j), i = lane - q * WP_SLABS;  // this lane's slab of the tile
           const bool mine = i >= 0 && i < ns;
-          for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
-            const uint32_t slot = c % RS;
-            const bool zero = !KV8 && kv == 1 && w.zeroes(j);
-            const uint32_t bar = zero ? land + 8 * slot : r_full + 8 * slot;
+          if constexpr (KV8) {
+            const uint32_t ks = c % KS, fs = c % FS;
             if (lane == 0) {
-              if (c >= RS) ok = wait(r_empty + 8 * slot, ((c / RS) - 1) & 1, 100);
-              if (ok) mbar_arrive_expect_tx(bar, ns * TILE * D * (KV8 ? 1 : 2));
+              if (c >= KS) ok = wait(empty + 8 * ks, ((c / KS) - 1) & 1, 100);
+              if (ok) mbar_arrive_expect_tx(full + 8 * ks, ns * TILE * D);
             }
             ok = warp_ok(ok);  // also orders the expect_tx before the copies
             if (!ok) break;
-            on_land = (on_land & ~(1u << slot)) | (zero ? 1u << slot : 0u);
-            if (zero) land_par ^= 1u << slot;
-            const uint32_t dst = r_data + slot * (KV8 ? C::STG_TILE : C::KV_TILE);
-            if (mine) {
-              if constexpr (KV8) {
-                tma_load_2d(dst + i * TILE * 128, kv ? &tmv : &tmk, 0, row, bar);
-              } else if (kv == 0) {
+            if (mine) tma_load_2d(ring + ks * C::F8_TILE + i * TILE * 128, &tmk, 0, row, full + 8 * ks);
+            if (lane == 0) {
+              if (c >= FS) ok = wait(sf_empty + 8 * fs, ((c / FS) - 1) & 1, 110);
+              if (ok) mbar_arrive_expect_tx(sf_full + 8 * fs, ns * TILE * D);
+            }
+            ok = warp_ok(ok);
+            if (!ok) {
+              ++c;  // K is on its way
+              break;
+            }
+            if (mine) tma_load_2d(smem_u32(stg_p) + fs * C::F8_TILE + i * TILE * 128, &tmv, 0, row, sf_full + 8 * fs);
+            ++c;
+          } else {
+            for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
+              const uint32_t slot = c % KS;
+              const bool zero = kv == 1 && w.zeroes(j);
+              const uint32_t bar = zero ? land + 8 * slot : full + 8 * slot;
+              if (lane == 0) {
+                if (c >= KS) ok = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 100);
+                if (ok) mbar_arrive_expect_tx(bar, ns * TILE * D * 2);
+              }
+              ok = warp_ok(ok);
+              if (!ok) break;
+              on_land = (on_land & ~(1u << slot)) | (zero ? 1u << slot : 0u);
+              if (zero) land_par ^= 1u << slot;
+              const uint32_t dst = ring + slot * C::KV_TILE;
+              if (mine) {
+                if (kv == 0) {
 #pragma unroll
-                for (int h = 0; h < C::NCH; ++h)
-                  tma_load_2d(dst + h * (WP_KEYS * 128) + i * TILE * 128, &tmk, 64 * h, row, bar);
-              } else if constexpr (D == 128) {
-                tma_load_3d(dst + i * 2 * TILE * 128, &tmv, 0, row, 0, bar);
-              } else {
-                tma_load_2d(dst + i * TILE * 128, &tmv, 0, row, bar);
+                  for (int h = 0; h < C::NCH; ++h)
+                    tma_load_2d(dst + h * (WP_KEYS * 128) + i * TILE * 128, &tmk, 64 * h, row, bar);
+                } else if constexpr (D == 128) {
+                  tma_load_3d(dst + i * 2 * TILE * 128, &tmv, 0, row, 0, bar);
+                } else {
+                  tma_load_2d(dst + i * TILE * 128, &tmv, 0, row, bar);
+                }
               }
             }
           }
         }
       }
-      if (*abort_flag && lane == 0)  // copies may still be landing in the last ring's slots
-        for (uint32_t k = c > RS ? c - RS : 0; k < c; ++k) {
-          const uint32_t slot = k % RS;
+      if (*abort_flag && lane == 0) {  // copies may still be landing in the rings' last slots
+        for (uint32_t k = c > KS ? c - KS : 0; k < c; ++k) {
+          const uint32_t slot = k % KS;
           if (!KV8 && (on_land >> slot & 1)) settle(land + 8 * slot, ~(land_par >> slot) & 1);
-          else settle(r_full + 8 * slot, (k / RS) & 1);
+          else settle(full + 8 * slot, (k / KS) & 1);
         }
+        if constexpr (KV8)
+          for (uint32_t k = c > FS ? c - FS : 0; k < c; ++k) settle(sf_full + 8 * (k % FS), (k / FS) & 1);
+      }
     } else if (warp == 9 || warp == 11) {
       // ------------------------------------------------------------ the products of tile X (9: A, 11: B)
       // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
@@ -413,9 +458,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // operand descriptors: the first, and a step of the address field (16-byte units) from there on
       const uint64_t q_desc = umma_desc_sw128(uni(qs) + X * C::Q_TILE, 16, 1024);
       const uint64_t k_desc = umma_desc_sw128(uni(ring), 16, 1024);
-      const uint64_t v_desc = umma_desc_sw128(uni(ring), TILE * 128, 1024);
+      const uint64_t v_desc = umma_desc_sw128(uni(KV8 ? smem_u32(vop_p) : ring), TILE * 128, 1024);
       const uint32_t bars = uni(q_full);  // the barriers from here on
       const uint32_t u_empty = bars + (empty - q_full), u_q_empty = bars + 16;
+      const uint32_t u_v_empty = bars + ((KV8 ? vo_empty : empty) - q_full);
       const uint32_t u_s_full = bars + (s_full - q_full) + 8 * X, u_o_full = bars + (o_full - q_full) + 8 * X;
       const uint32_t u_turn = bars + (turn - q_full) + 8 * (1 - X);  // the other tile's
       auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
@@ -424,7 +470,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       auto commit = [&](uint32_t bar) {
         if (elect_one()) umma_commit(bar);
       };
-      uint32_t c = 0, items = 0, np = 0, turns = 0;  // ring position; items; P tiles taken; turns had
+      constexpr uint32_t VS_ = VS > 0 ? VS : 1;
+      uint32_t c = 0, vc = 0, items = 0, np = 0, turns = 0;  // ring positions; items; P tiles taken; turns had
       while (ok && next_item(w)) {
         if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
         const bool live = uni(X < w.nq) != 0;
@@ -433,10 +480,11 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         for (int i = -1; i < nt && ok; ++i) {  // P V of the item's i-th key tile, then Q K of the next
           // everything is waited for before the turn: within it the products follow each other without a gap
           const bool has_pv = i >= 0, has_qk = i + 1 < nt;
-          const uint32_t vs = c % KS, ks = (c + has_pv) % KS;
+          // 16-bit pools: ring position c, V and K tiles in turn; E4M3 pools: key tile c of each of the two rings
+          const uint32_t vs = KV8 ? vc % VS_ : c % KS, ks = (KV8 ? c : c + has_pv) % KS;
           if (has_pv) {
-            ok = wait_all(full + 8 * vs, (c / KS) & 1, 210);
-            ++c;
+            ok = KV8 ? wait_all(vo_full + 8 * vs, (vc / VS_) & 1, 210) : wait_all(full + 8 * vs, (c / KS) & 1, 210);
+            if (KV8) ++vc; else ++c;
           }
           if (ok && has_qk) {
             ok = wait_all(full + 8 * ks, (c / KS) & 1, 220);
@@ -447,10 +495,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (!ok) break;
           ++turns;
           tc_fence_after();
-          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * (C::KV_TILE / 16);
+          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * ((KV8 ? C::F8_TILE : C::KV_TILE) / 16);
           const int nv = has_pv ? min(WP_SLABS, nslab - i * WP_SLABS) : 0;
-          const uint32_t idesc_s =
-              umma_idesc_f16(BF16, 128, has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE, false);
+          const int nk = has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE;
+          const uint32_t idesc_s = KV8 ? umma_idesc_e4m3(128, nk) : umma_idesc_f16(BF16, 128, nk, false);
           // P of keys 0 .. 31 and 64 .. 127 comes first (slabs 0, 1, 4 .. 7; slab 0 is always there)
           auto pv = [&](int k) {
             if (k < nv)
@@ -473,11 +521,13 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               for (int k = 2; k < 4; ++k) pv(k);
               if (has_qk) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {  // 64-wide chunk; 16 elements along its 128-byte row
+                for (int k = 0; k < D / 16; ++k) {
                   // the other tile's warp is let go two products early, which hides its start
                   if (k == D / 16 - 2) mbar_arrive(u_turn);
-                  umma_ss(s_tm, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
-                          kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
+                  // 16-bit: 64-wide chunk k / 4; 32 bytes along its 128-byte row.  E4M3: part k / 4 of q; all of d is one row
+                  const uint64_t qk = q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16;
+                  if constexpr (KV8) umma_f8(s_tm, qk, kd + (k & 3) * 2, idesc_s, k > 0);
+                  else umma_ss(s_tm, qk, kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
                 }
                 umma_commit(u_s_full);
               } else {
@@ -485,12 +535,12 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
                 umma_commit(u_o_full);
               }
               // this tile's use of the operands is over once its products so far are done
-              if (has_pv) umma_commit(u_empty + 8 * vs);
+              if (has_pv) umma_commit(u_v_empty + 8 * vs);
               if (has_qk) umma_commit(u_empty + 8 * ks);
               if (i + 2 == nt) umma_commit(u_q_empty);
             } else {
               mbar_arrive(u_turn);
-              if (has_pv) mbar_arrive(u_empty + 8 * vs);
+              if (has_pv) mbar_arrive(u_v_empty + 8 * vs);
               if (has_qk) mbar_arrive(u_empty + 8 * ks);
               if (i + 2 == nt) mbar_arrive(u_q_empty);
             }
@@ -568,35 +618,65 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   } else if (warp >= 12) {
     // -------------------------------------------------------------- E4M3: q and the staged codes to binary16
     if constexpr (KV8) {
-      // warps 12-15: q of tile A, then the K tiles; 16-19: q of B, the V tiles
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_CONVERT));
-      const int r = tid & 127, kv = warp >= 16;
-      uint32_t c = kv, items = 0;
+      const int r = tid & 127;
+      uint32_t c = 0, items = 0;
       while (ok && next_item(w)) {
         if (w.j0 == w.j1) continue;
-        ok = __all_sync(0xffffffffu, wait(q_full, items++ & 1, 500));
+        ok = __all_sync(0xffffffffu, wait(q_full, items & 1, 500));
         if (!ok) break;
-        uint4* qt = reinterpret_cast<uint4*>(base + kv * C::Q_TILE);
-        if (kv < w.nq)
-#pragma unroll 4
-          for (int k = r; k < C::Q_TILE / 16; k += 128) {
-            uint4 v = qt[k];
-            v = make_uint4(f16_of_bf16(v.x), f16_of_bf16(v.y), f16_of_bf16(v.z), f16_of_bf16(v.w));
-            qt[k] = v;
+        // Row r of each tile, 128 bf16 in two 128-byte rows of eight 16-byte units (unit u at u ^ (r & 7)), scaled by a power
+        // of two that brings its largest element to [128, 256), becomes x = hi + lo, both E4M3, 128 bytes each in the
+        // same two places: bf16 has 8 significant bits and E4M3 4, so the rest after hi is an E4M3 number again, down to
+        // 2^-10 (2^-17 of the row's largest).
+        for (int x = 0; x < w.nq; ++x) {
+          uint8_t* qr = base + x * C::Q_TILE + r * 128;
+          uint32_t mx = 0;  // the largest magnitude as bf16 bits, two side by side
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const uint4 v = *reinterpret_cast<const uint4*>(qr + (u >> 3) * 16384 + (((u & 7) ^ (r & 7)) << 4));
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
           }
+          mx = max(mx & 0xffffu, mx >> 16);
+          // a row with an infinity or a NaN is NaN throughout (0 times it is)
+          const int e = max(-120, min(120, 134 - static_cast<int>(mx >> 7)));
+          const float f = mx >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          q_exp[(items & 1) * 256 + x * 128 + r] = static_cast<int8_t>(e);
+          uint4 hi[8], lo[8];  // all read before any is written
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const uint4 v = *reinterpret_cast<const uint4*>(qr + (u >> 3) * 16384 + (((u & 7) ^ (r & 7)) << 4));
+            const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              e4m3_split(__uint_as_float(p[k] << 16) * f, __uint_as_float(p[k] & 0xffff0000u) * f, h[k], l[k]);
+            uint32_t* ho = &hi[u >> 1].x + 2 * (u & 1);
+            uint32_t* lw = &lo[u >> 1].x + 2 * (u & 1);
+            ho[0] = h[0] | h[1] << 16, ho[1] = h[2] | h[3] << 16;
+            lw[0] = l[0] | l[1] << 16, lw[1] = l[2] | l[3] << 16;
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            *reinterpret_cast<uint4*>(qr + ((u ^ (r & 7)) << 4)) = hi[u];
+            *reinterpret_cast<uint4*>(qr + 16384 + ((u ^ (r & 7)) << 4)) = lo[u];
+          }
+        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        for (int j = w.j0; j < w.j1 && ok; ++j, c += 2) {
-            const uint32_t f = c % FS, slot = c % KS;
-            bool here = wait(sf_full + 8 * f, (c / FS) & 1, 510);
-            if (here && c >= KS) here = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 520);
+        ++items;
+        for (int j = w.j0; j < w.j1 && ok; ++j, ++c) {
+            const uint32_t f = c % 2, slot = c % 2;
+            bool here = wait(sf_full + 8 * f, (c / 2) & 1, 510);
+            if (here && c >= 2) here = wait(vo_empty + 8 * slot, ((c / 2) - 1) & 1, 520);
             ok = __all_sync(0xffffffffu, here);
             if (!ok) break;
-            const uint8_t* src = stg_p + f * C::STG_TILE;
-            uint8_t* dst = ring_p + slot * C::KV_TILE;
+            const uint8_t* src = stg_p + f * C::F8_TILE;
+            uint8_t* dst = vop_p + slot * C::KV_TILE;
             const int ns = w.slabs_of(j);
-            const bool zero = kv == 1 && w.zeroes(j);
+            const bool zero = w.zeroes(j);
             // staging row rr of slab i holds d = 16 u .. 16 u + 15 in 16-byte unit u ^ (rr & 7); the operand rows hold
             // d in two 64-wide chunks of eight units, unit t at t ^ (row & 7).  Thread r: row r / 8, unit r % 8 of slab i
             const int rr = r >> 3, u = r & 7, cc = u >> 2, t = (u & 3) * 2, sw = rr & 7;
@@ -609,15 +689,14 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               f16_of_e4m3(v.z, o1.x, o1.y);
               f16_of_e4m3(v.w, o1.z, o1.w);
               if (zero && w.hidden(w.slab(j * WP_SLABS + i) * TILE + rr)) o0 = o1 = make_uint4(0, 0, 0, 0);
-              uint8_t* p = kv == 0 ? dst + cc * (WP_KEYS * 128) + (i * TILE + rr) * 128
-                                   : dst + i * (2 * TILE * 128) + cc * (TILE * 128) + rr * 128;
+              uint8_t* p = dst + i * (2 * TILE * 128) + cc * (TILE * 128) + rr * 128;
               *reinterpret_cast<uint4*>(p + ((t ^ sw) << 4)) = o0;
               *reinterpret_cast<uint4*>(p + (((t + 1) ^ sw) << 4)) = o1;
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(full + 8 * slot);
+              mbar_arrive(vo_full + 8 * slot);
               mbar_arrive(sf_empty + 8 * f);
             }
           }
@@ -629,19 +708,21 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
-    const float sl = a.scale_log2;
-    uint32_t n_s = 0, no = 0;  // S tiles and outputs taken
+    uint32_t n_s = 0, no = 0, items = 0;  // S tiles and outputs taken; items
     while (ok && next_item(w)) {
+      const uint32_t item = w.j0 < w.j1 ? items++ : 0;
       if (X >= w.nq) continue;
       const int qi = w.i0 + X * QB + r / G;
       const bool valid = r < QB * G && qi < w.i1;
       const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, sl = a.scale_log2;
       for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
         ok = __all_sync(0xffffffffu, wait(s_full + 8 * X, n_s & 1, 600));
         if (!ok) break;
         tc_fence_after();
+        if (KV8 && j == w.j0)  // the row's q is scaled by 2^e
+          sl *= __uint_as_float(static_cast<uint32_t>(127 - q_exp[(item & 1) * 256 + X * 128 + r]) << 23);
         uint32_t sa[2][32], sb[2][32];  // the first 64 keys and the others
         tmem_ld32(s_addr, sa[0]);
         tmem_ld32(s_addr + 32, sa[1]);
