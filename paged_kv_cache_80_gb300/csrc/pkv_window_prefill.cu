@@ -17,8 +17,7 @@
 //
 // Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 and 11
 // issue the products of A and of B; 10 loads Q and zeroes V rows that no row sees (0 times whatever lies there must
-// stay 0).  E4M3 pools: K codes are an operand as they are, with q as the sum of two E4M3 numbers (two products at
-// twice the rate), and V codes are converted to binary16, both by warps 12-15.
+// stay 0).  E4M3 pools: 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16.
 // TMEM: S of A and B (128 columns each; P overwrites its last 64), O of A and B from column 256 on.
 // A tile's products are issued by one thread and taken in order, ..., P V(j), Q K(j + 1), ...: S(j + 1) may go over
 // P(j), and its arrival says that O holds P V(j).
@@ -42,27 +41,26 @@ namespace pkv {
 
 namespace {
 
-constexpr int WP_KEYS = 128, WP_SLABS = WP_KEYS / TILE;
+constexpr int WP_TBL = 256;  // entries of the table that finds an item's sequence
 
 template <bool KV8, int D>
 struct WpCfg {
-  static constexpr int THREADS = KV8 ? 512 : 384;
-  static constexpr int TBL = KV8 ? 128 : 256;             // entries of the table that finds an item's sequence
+  static constexpr int THREADS = KV8 ? 640 : 384;
+  static constexpr int KEYS = KV8 ? 64 : 128, SLABS = KEYS / TILE;  // a key tile
   static constexpr int NCH = D / 64;                      // 64-wide chunks of d (128 bytes, the swizzle's width)
-  static constexpr int Q_TILE = 128 * D * 2;              // one Q tile (E4M3: its two parts, below)
-  static constexpr int KV_TILE = WP_KEYS * D * 2;         // one K or V tile of 16-bit operands
-  static constexpr int F8_TILE = WP_KEYS * D;             // one of E4M3 codes
-  // 16-bit pools: one ring of KS operands, K and V tiles in turn.  E4M3 pools: KS K tiles, FS staged V tiles and VS
-  // converted ones.
-  static constexpr int KS = KV8 ? 4 : (D == 64 ? 8 : 5), FS = KV8 ? 2 : 0, VS = KV8 ? 2 : 0;
-  static constexpr int DATA = 2 * Q_TILE + (KV8 ? KS * F8_TILE + VS * KV_TILE + FS * F8_TILE : KS * KV_TILE);
-  static constexpr int BARS = 3 + 3 * KS + 6 * 2 + 4 + 2 * FS + 2 * VS;
+  static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
+  static constexpr int KV_TILE = KEYS * D * 2;         // one K or V tile as an operand (16-bit)
+  static constexpr int STG_TILE = KEYS * D;            // one K or V tile of E4M3 codes
+  static constexpr int KS = KV8 ? 6 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
+  static constexpr int FS = KV8 ? 8 : 0;                  // staging ring
+  static constexpr int BARS = 3 + 3 * KS + 2 * 4 + 5 * 2 + 4 + 2 * FS;
   static constexpr int READERS = THREADS / 32 - 1;        // warps that follow the items
-  static constexpr int SMEM = 1024 + DATA + (BARS + 1) * 8 + 16 + 2 * 64 + 96 + (TBL + 1) * 4 + (KV8 ? 512 : 0);
+  static constexpr int DATA = 2 * Q_TILE + KS * KV_TILE + FS * STG_TILE;
+  static constexpr int SMEM = 1024 + DATA + (BARS + 1) * 8 + 16 + 2 * 64 + 96 + (WP_TBL + 1) * 4;
   // registers: the launch's share is 65,536 / THREADS rounded down to a multiple of 8
-  static constexpr int R_LAUNCH = KV8 ? 128 : 168;
-  static constexpr int R_SOFTMAX = KV8 ? 168 : 208, R_CONTROL = KV8 ? 72 : 88, R_CONVERT = 96;
-  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 128 * R_CONVERT : 0) <= THREADS * R_LAUNCH, "register split");
+  static constexpr int R_LAUNCH = KV8 ? 96 : 168;
+  static constexpr int R_SOFTMAX = KV8 ? 160 : 208, R_CONTROL = KV8 ? 64 : 88, R_CONVERT = 48;
+  static_assert(256 * R_SOFTMAX + 128 * R_CONTROL + (KV8 ? 256 * R_CONVERT : 0) <= THREADS * R_LAUNCH, "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -106,32 +104,16 @@ __device__ __forceinline__ uint32_t below(int n) {
   return (1u << k) - 1u;
 }
 
-// four E4M3 codes to binary16 (exact), the first of each pair low
+// four E4M3 codes to binary16 (exact), and two bfloat16 rounded to binary16, the first of each pair low
 __device__ __forceinline__ void f16_of_e4m3(uint32_t x, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
 }
-// two values to E4M3 codes (the first low), and the rest that the codes leave of them, as codes
-__device__ __forceinline__ void e4m3_split(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-  uint32_t h2;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(h2) : "r"(hi));
-  const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(x - back.x, y - back.y), __NV_SATFINITE, __NV_E4M3);
-}
-
-// D(tmem) (+)= A(smem) B(smem)^T on 8-bit operands, K = 32
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor of kind::f8f6f4: binary32 accumulator, A and B both E4M3 (format 0) and K-major
-__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t x) {
+  const __half2 h = __floats2half2_rn(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
@@ -145,7 +127,8 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // One item: where its rows and keys are (16 words: it travels through shared memory).
-struct __align__(16) Item {
+template <int SLABS>
+struct __align__(16) ItemT {
   int32_t s, g;
   int32_t qbeg, i0, i1, nq;              // chunk's first row; its queries i0 .. i1 - 1; tiles with rows (1, 2)
   int32_t P, nkeys;                      // position of query 0; keys up to the last query
@@ -154,7 +137,7 @@ struct __align__(16) Item {
   int32_t j0, j1;                        // this CTA's key tiles
   int32_t work;                          // 0: no item (any more)
   __device__ __forceinline__ int32_t slab(int32_t u) const { return u < sink_slabs ? u : first + u - sink_slabs; }
-  __device__ __forceinline__ int32_t slabs_of(int32_t j) const { return min(WP_SLABS, nslab - j * WP_SLABS); }
+  __device__ __forceinline__ int32_t slabs_of(int32_t j) const { return min(SLABS, nslab - j * SLABS); }
   __device__ __forceinline__ bool hidden(int32_t t) const { return t >= nkeys || (t >= sink_end && t < lo); }
   __device__ __forceinline__ bool ragged(int32_t u) const {  // slab u holds a key hidden from every row
     return hidden(slab(u) * TILE) || hidden(slab(u) * TILE + TILE - 1) ||
@@ -162,7 +145,7 @@ struct __align__(16) Item {
   }
   // tile j holds such a slab: only the last with sinks, the first after them and the last can
   __device__ __forceinline__ bool zeroes(int32_t j) const {
-    const int32_t a = j * WP_SLABS, b = a + slabs_of(j);
+    const int32_t a = j * SLABS, b = a + slabs_of(j);
     auto at = [&](int32_t u) { return u >= a && u < b && ragged(u); };
     return at(sink_slabs - 1) || at(sink_slabs) || at(nslab - 1);
   }
@@ -174,9 +157,11 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmv, const DecodeArgs a, const int32_t* __restrict__ q_off,
                        int32_t max_q, int32_t csize, int64_t most_items) {
   using C = WpCfg<KV8, D>;
-  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // type of P and V as operands
+  using Item = ItemT<C::SLABS>;
+  constexpr int WP_KEYS = C::KEYS, WP_SLABS = C::SLABS;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value && !KV8;  // operand type of the products
   using TP = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr int KS = C::KS, FS = C::FS, VS = C::VS;
+  constexpr int KS = C::KS, FS = C::FS;
   extern __shared__ uint8_t smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.G, QB = 128 / G;  // queries a tile
@@ -185,38 +170,39 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t qs = smem_u32(base), ring = qs + 2 * C::Q_TILE;
   uint8_t* ring_p = base + 2 * C::Q_TILE;
-  uint8_t* vop_p = ring_p + KS * C::F8_TILE;  // E4M3: converted V tiles, then staged ones
-  uint8_t* stg_p = vop_p + VS * C::KV_TILE;
+  uint8_t* stg_p = ring_p + KS * C::KV_TILE;
   uint8_t* bar_p = base + C::DATA;
   const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
-  // per tile A, B: S; the first three quarters of P, all of it; the item's O; the turn to issue; after an abort
-  const uint32_t s_full = land + 8 * KS, p_most = s_full + 16, p_full = p_most + 16, o_full = p_full + 16;
-  const uint32_t turn = o_full + 16, drain = turn + 16;
-  const uint32_t sf_full = drain + 16, sf_empty = sf_full + 8 * FS;             // staged V (E4M3)
-  const uint32_t vo_full = sf_empty + 8 * FS, vo_empty = vo_full + 8 * VS;      // converted V
-  const uint32_t it_full = vo_empty + 8 * VS, it_empty = it_full + 16;          // items, two places
+  // per tile A, B: S and P (E4M3: of an even and of an odd key tile); three quarters of P, P V done; the item's O done;
+  // the turn to issue; after an abort
+  const uint32_t s_full = land + 8 * KS, p_full = s_full + 32, p_most = p_full + 32, o_done = p_most + 16;
+  const uint32_t o_full = o_done + 16, turn = o_full + 16, drain = turn + 16;
+  const uint32_t sf_full = drain + 16, sf_empty = sf_full + 8 * FS;  // staging ring
+  const uint32_t it_full = sf_full + 16 * FS, it_empty = it_full + 16;  // items, two places
   uint8_t* tail_p = bar_p + (C::BARS + 1) / 2 * 16;
   Item* items_p = reinterpret_cast<Item*>(tail_p);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(tail_p + 2 * sizeof(Item));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int32_t* wsum = reinterpret_cast<int32_t*>(tslot + 4);
-  int8_t* q_exp = reinterpret_cast<int8_t*>(wsum + 24);  // E4M3: exponents of the rows' q, of two items in turn
-  int32_t* pre = wsum + 24 + (KV8 ? 128 : 0);  // [groups + 1]: query-block pairs of the sequences before a group of them
+  int32_t* pre = wsum + 24;  // [groups + 1]: query-block pairs of the sequences before a group of them
 
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_ready, 4);  // one arrival a warp
+    mbar_init(q_ready, 8);  // one arrival a warp
     mbar_init(q_empty, 2);
     for (int k = 0; k < KS; ++k) {
-      mbar_init(full + 8 * k, 1);
+      mbar_init(full + 8 * k, KV8 ? 4 : 1);
       mbar_init(empty + 8 * k, 2);  // both tiles' products
       mbar_init(land + 8 * k, 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(s_full + 8 * x, 1);
-      mbar_init(p_most + 8 * x, 4);  // one arrival a warp
-      mbar_init(p_full + 8 * x, 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(s_full + 16 * x + 8 * b, 1);
+        mbar_init(p_full + 16 * x + 8 * b, 4);  // one arrival a warp
+      }
+      mbar_init(p_most + 8 * x, 4);
+      mbar_init(o_done + 8 * x, 1);
       mbar_init(turn + 8 * x, 1);
       mbar_init(o_full + 8 * x, 1);
       mbar_init(drain + 8 * x, 1);
@@ -224,10 +210,6 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     for (int k = 0; k < FS; ++k) {
       mbar_init(sf_full + 8 * k, 1);
       mbar_init(sf_empty + 8 * k, 4);
-    }
-    for (int k = 0; k < VS; ++k) {
-      mbar_init(vo_full + 8 * k, 4);
-      mbar_init(vo_empty + 8 * k, 2);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(it_full + 8 * k, 1);
@@ -239,9 +221,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   if (warp == 8) tmem_alloc(smem_u32(tslot), 512);
 
   // ---- the items, counted ahead so that ragged chunks leave no holes: a thread counts the query-block pairs of
-  // `per` sequences (one, up to C::TBL of them), and the table holds the sums before each such group
+  // `per` sequences (one, up to WP_TBL of them), and the table holds the sums before each such group
   const int most = (max_q + 2 * QB - 1) / (2 * QB);  // query-block pairs of a chunk at most
-  const int per = (a.n_seq + C::TBL - 1) / C::TBL, groups = (a.n_seq + per - 1) / per;
+  const int per = (a.n_seq + WP_TBL - 1) / WP_TBL, groups = (a.n_seq + per - 1) / per;
   auto pairs_of = [&](int s, bool record) -> int {
     const int q0 = q_off[s], c = q_off[s + 1] - q0;
     if (q0 < 0 || c < 0 || c > a.n_tok - q0) {
@@ -360,8 +342,11 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // Lane i holds the pool row of slab 32 k + i of the list (the next 32 are looked up ahead); the 8 lanes of tile
       // j copy its slabs.  16-bit pools: a K slab as one box per 64-wide chunk ([chunk][128 keys][128 B]), a V slab
       // as one box of all chunks ([slab][chunk][16 keys][128 B]); E4M3 pools: 2 KB of codes into the staging ring.
-      uint32_t c = 0;  // tiles loaded so far (E4M3: pairs of them)
-      uint32_t on_land = 0;  // of the last KS tiles, those whose bytes arrive at `land` (bit c % KS)
+      constexpr int RS = KV8 ? FS : KS;
+      const uint32_t r_full = KV8 ? sf_full : full, r_empty = KV8 ? sf_empty : empty;
+      const uint32_t r_data = KV8 ? smem_u32(stg_p) : ring;
+      uint32_t c = 0;  // tiles loaded so far
+      uint32_t on_land = 0;  // of the last RS tiles, those whose bytes arrive at `land` (bit c % RS)
       uint32_t land_par = 0;  // bit k: parity of the uses of `land` slot k
       while (ok && next_item(w)) {
         auto row_of = [&](int u) -> int {
@@ -385,64 +370,41 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           }
           const int ns = w.slabs_of(j), i = lane - q * WP_SLABS;  // this lane's slab of the tile
           const bool mine = i >= 0 && i < ns;
-          if constexpr (KV8) {
-            const uint32_t ks = c % KS, fs = c % FS;
+          for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
+            const uint32_t slot = c % RS;
+            const bool zero = !KV8 && kv == 1 && w.zeroes(j);
+            const uint32_t bar = zero ? land + 8 * slot : r_full + 8 * slot;
             if (lane == 0) {
-              if (c >= KS) ok = wait(empty + 8 * ks, ((c / KS) - 1) & 1, 100);
-              if (ok) mbar_arrive_expect_tx(full + 8 * ks, ns * TILE * D);
+              if (c >= RS) ok = wait(r_empty + 8 * slot, ((c / RS) - 1) & 1, 100);
+              if (ok) mbar_arrive_expect_tx(bar, ns * TILE * D * (KV8 ? 1 : 2));
             }
             ok = warp_ok(ok);  // also orders the expect_tx before the copies
             if (!ok) break;
-            if (mine) tma_load_2d(ring + ks * C::F8_TILE + i * TILE * 128, &tmk, 0, row, full + 8 * ks);
-            if (lane == 0) {
-              if (c >= FS) ok = wait(sf_empty + 8 * fs, ((c / FS) - 1) & 1, 110);
-              if (ok) mbar_arrive_expect_tx(sf_full + 8 * fs, ns * TILE * D);
-            }
-            ok = warp_ok(ok);
-            if (!ok) {
-              ++c;  // K is on its way
-              break;
-            }
-            if (mine) tma_load_2d(smem_u32(stg_p) + fs * C::F8_TILE + i * TILE * 128, &tmv, 0, row, sf_full + 8 * fs);
-            ++c;
-          } else {
-            for (int kv = 0; kv < 2 && ok; ++kv, ++c) {
-              const uint32_t slot = c % KS;
-              const bool zero = kv == 1 && w.zeroes(j);
-              const uint32_t bar = zero ? land + 8 * slot : full + 8 * slot;
-              if (lane == 0) {
-                if (c >= KS) ok = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 100);
-                if (ok) mbar_arrive_expect_tx(bar, ns * TILE * D * 2);
-              }
-              ok = warp_ok(ok);
-              if (!ok) break;
-              on_land = (on_land & ~(1u << slot)) | (zero ? 1u << slot : 0u);
-              if (zero) land_par ^= 1u << slot;
-              const uint32_t dst = ring + slot * C::KV_TILE;
-              if (mine) {
-                if (kv == 0) {
+            on_land = (on_land & ~(1u << slot)) | (zero ? 1u << slot : 0u);
+            if (zero) land_par ^= 1u << slot;
+            const uint32_t dst = r_data + slot * (KV8 ? C::STG_TILE : C::KV_TILE);
+            if (mine) {
+              if constexpr (KV8) {
+                tma_load_2d(dst + i * TILE * 128, kv ? &tmv : &tmk, 0, row, bar);
+              } else if (kv == 0) {
 #pragma unroll
-                  for (int h = 0; h < C::NCH; ++h)
-                    tma_load_2d(dst + h * (WP_KEYS * 128) + i * TILE * 128, &tmk, 64 * h, row, bar);
-                } else if constexpr (D == 128) {
-                  tma_load_3d(dst + i * 2 * TILE * 128, &tmv, 0, row, 0, bar);
-                } else {
-                  tma_load_2d(dst + i * TILE * 128, &tmv, 0, row, bar);
-                }
+                for (int h = 0; h < C::NCH; ++h)
+                  tma_load_2d(dst + h * (WP_KEYS * 128) + i * TILE * 128, &tmk, 64 * h, row, bar);
+              } else if constexpr (D == 128) {
+                tma_load_3d(dst + i * 2 * TILE * 128, &tmv, 0, row, 0, bar);
+              } else {
+                tma_load_2d(dst + i * TILE * 128, &tmv, 0, row, bar);
               }
             }
           }
         }
       }
-      if (*abort_flag && lane == 0) {  // copies may still be landing in the rings' last slots
-        for (uint32_t k = c > KS ? c - KS : 0; k < c; ++k) {
-          const uint32_t slot = k % KS;
+      if (*abort_flag && lane == 0)  // copies may still be landing in the last ring's slots
+        for (uint32_t k = c > RS ? c - RS : 0; k < c; ++k) {
+          const uint32_t slot = k % RS;
           if (!KV8 && (on_land >> slot & 1)) settle(land + 8 * slot, ~(land_par >> slot) & 1);
-          else settle(full + 8 * slot, (k / KS) & 1);
+          else settle(r_full + 8 * slot, (k / RS) & 1);
         }
-        if constexpr (KV8)
-          for (uint32_t k = c > FS ? c - FS : 0; k < c; ++k) settle(sf_full + 8 * (k % FS), (k / FS) & 1);
-      }
     } else if (warp == 9 || warp == 11) {
       // ------------------------------------------------------------ the products of tile X (9: A, 11: B)
       // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
@@ -458,11 +420,11 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // operand descriptors: the first, and a step of the address field (16-byte units) from there on
       const uint64_t q_desc = umma_desc_sw128(uni(qs) + X * C::Q_TILE, 16, 1024);
       const uint64_t k_desc = umma_desc_sw128(uni(ring), 16, 1024);
-      const uint64_t v_desc = umma_desc_sw128(uni(KV8 ? smem_u32(vop_p) : ring), TILE * 128, 1024);
+      const uint64_t v_desc = umma_desc_sw128(uni(ring), TILE * 128, 1024);
       const uint32_t bars = uni(q_full);  // the barriers from here on
       const uint32_t u_empty = bars + (empty - q_full), u_q_empty = bars + 16;
-      const uint32_t u_v_empty = bars + ((KV8 ? vo_empty : empty) - q_full);
-      const uint32_t u_s_full = bars + (s_full - q_full) + 8 * X, u_o_full = bars + (o_full - q_full) + 8 * X;
+      const uint32_t u_s_full = bars + (s_full - q_full) + 16 * X, u_o_full = bars + (o_full - q_full) + 8 * X;
+      const uint32_t u_o_done = bars + (o_done - q_full) + 8 * X;
       const uint32_t u_turn = bars + (turn - q_full) + 8 * (1 - X);  // the other tile's
       auto wait_all = [&](uint32_t bar, uint32_t parity, int where) {
         return __all_sync(0xffffffffu, wait(bar, parity, where)) != 0;
@@ -470,21 +432,78 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       auto commit = [&](uint32_t bar) {
         if (elect_one()) umma_commit(bar);
       };
-      constexpr uint32_t VS_ = VS > 0 ? VS : 1;
-      uint32_t c = 0, vc = 0, items = 0, np = 0, turns = 0;  // ring positions; items; P tiles taken; turns had
+      uint32_t c = 0, items = 0, ns_ = 0, np = 0, turns = 0;  // ring position; items; S and P tiles; turns had
       while (ok && next_item(w)) {
         if (w.j0 == w.j1) continue;  // a cluster rank without a key tile
         const bool live = uni(X < w.nq) != 0;
         const int nt = uni(w.j1 - w.j0), nslab = uni(w.nslab - w.j0 * WP_SLABS);
         ok = wait_all(KV8 ? q_ready : q_full, items++ & 1, 200);
+        if constexpr (KV8) {
+          // S of the item's i-th key tile (its K is at ring position c + 2 i)
+          auto qk = [&](int i) -> bool {
+            const uint32_t at = c + 2 * i, slot = at % KS;
+            if (!wait_all(full + 8 * slot, (at / KS) & 1, 210)) return false;
+            tc_fence_after();
+            const uint64_t kd = k_desc + slot * (C::KV_TILE / 16);
+            const uint32_t idesc_s = umma_idesc_f16(BF16, 128, min(WP_SLABS, nslab - i * WP_SLABS) * TILE, false);
+            const uint32_t b = ns_ & 1;
+            if (elect_one()) {
+              if (live) {
+  #pragma unroll
+                for (int k = 0; k < D / 16; ++k)  // 64-wide chunk; 16 elements along its 128-byte row
+                  umma_ss(s_tm + 64 * b, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
+                          kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
+                umma_commit(u_s_full + 8 * b);
+                umma_commit(u_empty + 8 * slot);  // this tile's use of the operand is over once its products are done
+                if (i + 1 == nt) umma_commit(u_q_empty);
+              } else {
+                mbar_arrive(empty + 8 * slot);
+                if (i + 1 == nt) mbar_arrive(q_empty);
+              }
+            }
+            __syncwarp();
+            ++ns_;
+            return true;
+          };
+          auto pv = [&](int i) -> bool {
+            const uint32_t at = c + 2 * i + 1, slot = at % KS, b = np & 1;
+            if (!wait_all(full + 8 * slot, (at / KS) & 1, 220)) return false;
+            if (live && !wait_all(p_full + 16 * X + 8 * b, (np >> 1) & 1, 230)) return false;
+            tc_fence_after();
+            const uint64_t vd = v_desc + slot * (C::KV_TILE / 16);
+            const int n = min(WP_SLABS, nslab - i * WP_SLABS);
+            if (elect_one()) {
+              if (live) {
+  #pragma unroll
+                for (int k = 0; k < WP_SLABS; ++k)
+                  if (k < n)
+                    umma_ts(o_tm, s_tm + 64 * b + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+                umma_commit(u_o_done);
+                if (i + 1 == nt) umma_commit(u_o_full);
+                umma_commit(u_empty + 8 * slot);
+              } else {
+                mbar_arrive(empty + 8 * slot);
+              }
+            }
+            __syncwarp();
+            ++np;
+            return true;
+          };
+          if (ok) ok = qk(0);
+          for (int i = 0; i < nt && ok; ++i) {
+            if (i + 1 < nt) ok = qk(i + 1);
+            if (ok) ok = pv(i);
+          }
+          c += 2 * nt;
+          if (!live) ns_ -= nt, np -= nt;  // no S or P of this tile
+        } else
         for (int i = -1; i < nt && ok; ++i) {  // P V of the item's i-th key tile, then Q K of the next
           // everything is waited for before the turn: within it the products follow each other without a gap
           const bool has_pv = i >= 0, has_qk = i + 1 < nt;
-          // 16-bit pools: ring position c, V and K tiles in turn; E4M3 pools: key tile c of each of the two rings
-          const uint32_t vs = KV8 ? vc % VS_ : c % KS, ks = (KV8 ? c : c + has_pv) % KS;
+          const uint32_t vs = c % KS, ks = (c + has_pv) % KS;
           if (has_pv) {
-            ok = KV8 ? wait_all(vo_full + 8 * vs, (vc / VS_) & 1, 210) : wait_all(full + 8 * vs, (c / KS) & 1, 210);
-            if (KV8) ++vc; else ++c;
+            ok = wait_all(full + 8 * vs, (c / KS) & 1, 210);
+            ++c;
           }
           if (ok && has_qk) {
             ok = wait_all(full + 8 * ks, (c / KS) & 1, 220);
@@ -495,10 +514,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (!ok) break;
           ++turns;
           tc_fence_after();
-          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * ((KV8 ? C::F8_TILE : C::KV_TILE) / 16);
+          const uint64_t vd = v_desc + vs * (C::KV_TILE / 16), kd = k_desc + ks * (C::KV_TILE / 16);
           const int nv = has_pv ? min(WP_SLABS, nslab - i * WP_SLABS) : 0;
-          const int nk = has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE;
-          const uint32_t idesc_s = KV8 ? umma_idesc_e4m3(128, nk) : umma_idesc_f16(BF16, 128, nk, false);
+          const uint32_t idesc_s =
+              umma_idesc_f16(BF16, 128, has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE, false);
           // P of keys 0 .. 31 and 64 .. 127 comes first (slabs 0, 1, 4 .. 7; slab 0 is always there)
           auto pv = [&](int k) {
             if (k < nv)
@@ -511,7 +530,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
                 if (k < 2 || k >= 4) pv(k);
             }
             __syncwarp();
-            ok = wait_all(p_full + 8 * X, np++ & 1, 250);
+            ok = wait_all(p_full + 16 * X, np++ & 1, 250);
             if (!ok) break;
             tc_fence_after();
           }
@@ -521,13 +540,11 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               for (int k = 2; k < 4; ++k) pv(k);
               if (has_qk) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
+                for (int k = 0; k < D / 16; ++k) {  // 64-wide chunk; 16 elements along its 128-byte row
                   // the other tile's warp is let go two products early, which hides its start
                   if (k == D / 16 - 2) mbar_arrive(u_turn);
-                  // 16-bit: 64-wide chunk k / 4; 32 bytes along its 128-byte row.  E4M3: part k / 4 of q; all of d is one row
-                  const uint64_t qk = q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16;
-                  if constexpr (KV8) umma_f8(s_tm, qk, kd + (k & 3) * 2, idesc_s, k > 0);
-                  else umma_ss(s_tm, qk, kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
+                  umma_ss(s_tm, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
+                          kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
                 }
                 umma_commit(u_s_full);
               } else {
@@ -535,12 +552,12 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
                 umma_commit(u_o_full);
               }
               // this tile's use of the operands is over once its products so far are done
-              if (has_pv) umma_commit(u_v_empty + 8 * vs);
+              if (has_pv) umma_commit(u_empty + 8 * vs);
               if (has_qk) umma_commit(u_empty + 8 * ks);
               if (i + 2 == nt) umma_commit(u_q_empty);
             } else {
               mbar_arrive(u_turn);
-              if (has_pv) mbar_arrive(u_v_empty + 8 * vs);
+              if (has_pv) mbar_arrive(u_empty + 8 * vs);
               if (has_qk) mbar_arrive(u_empty + 8 * ks);
               if (i + 2 == nt) mbar_arrive(u_q_empty);
             }
@@ -618,65 +635,35 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   } else if (warp >= 12) {
     // -------------------------------------------------------------- E4M3: q and the staged codes to binary16
     if constexpr (KV8) {
+      // warps 12-15: q of tile A, then the K tiles; 16-19: q of B, the V tiles
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_CONVERT));
-      const int r = tid & 127;
-      uint32_t c = 0, items = 0;
+      const int r = tid & 127, kv = warp >= 16;
+      uint32_t c = kv, items = 0;
       while (ok && next_item(w)) {
         if (w.j0 == w.j1) continue;
-        ok = __all_sync(0xffffffffu, wait(q_full, items & 1, 500));
+        ok = __all_sync(0xffffffffu, wait(q_full, items++ & 1, 500));
         if (!ok) break;
-        // Row r of each tile, 128 bf16 in two 128-byte rows of eight 16-byte units (unit u at u ^ (r & 7)), scaled by a power
-        // of two that brings its largest element to [128, 256), becomes x = hi + lo, both E4M3, 128 bytes each in the
-        // same two places: bf16 has 8 significant bits and E4M3 4, so the rest after hi is an E4M3 number again, down to
-        // 2^-10 (2^-17 of the row's largest).
-        for (int x = 0; x < w.nq; ++x) {
-          uint8_t* qr = base + x * C::Q_TILE + r * 128;
-          uint32_t mx = 0;  // the largest magnitude as bf16 bits, two side by side
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const uint4 v = *reinterpret_cast<const uint4*>(qr + (u >> 3) * 16384 + (((u & 7) ^ (r & 7)) << 4));
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        uint4* qt = reinterpret_cast<uint4*>(base + kv * C::Q_TILE);
+        if (kv < w.nq)
+#pragma unroll 4
+          for (int k = r; k < C::Q_TILE / 16; k += 128) {
+            uint4 v = qt[k];
+            v = make_uint4(f16_of_bf16(v.x), f16_of_bf16(v.y), f16_of_bf16(v.z), f16_of_bf16(v.w));
+            qt[k] = v;
           }
-          mx = max(mx & 0xffffu, mx >> 16);
-          // a row with an infinity or a NaN is NaN throughout (0 times it is)
-          const int e = max(-120, min(120, 134 - static_cast<int>(mx >> 7)));
-          const float f = mx >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-          q_exp[(items & 1) * 256 + x * 128 + r] = static_cast<int8_t>(e);
-          uint4 hi[8], lo[8];  // all read before any is written
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const uint4 v = *reinterpret_cast<const uint4*>(qr + (u >> 3) * 16384 + (((u & 7) ^ (r & 7)) << 4));
-            const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              e4m3_split(__uint_as_float(p[k] << 16) * f, __uint_as_float(p[k] & 0xffff0000u) * f, h[k], l[k]);
-            uint32_t* ho = &hi[u >> 1].x + 2 * (u & 1);
-            uint32_t* lw = &lo[u >> 1].x + 2 * (u & 1);
-            ho[0] = h[0] | h[1] << 16, ho[1] = h[2] | h[3] << 16;
-            lw[0] = l[0] | l[1] << 16, lw[1] = l[2] | l[3] << 16;
-          }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            *reinterpret_cast<uint4*>(qr + ((u ^ (r & 7)) << 4)) = hi[u];
-            *reinterpret_cast<uint4*>(qr + 16384 + ((u ^ (r & 7)) << 4)) = lo[u];
-          }
-        }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        ++items;
-        for (int j = w.j0; j < w.j1 && ok; ++j, ++c) {
-            const uint32_t f = c % 2, slot = c % 2;
-            bool here = wait(sf_full + 8 * f, (c / 2) & 1, 510);
-            if (here && c >= 2) here = wait(vo_empty + 8 * slot, ((c / 2) - 1) & 1, 520);
+        for (int j = w.j0; j < w.j1 && ok; ++j, c += 2) {
+            const uint32_t f = c % FS, slot = c % KS;
+            bool here = wait(sf_full + 8 * f, (c / FS) & 1, 510);
+            if (here && c >= KS) here = wait(empty + 8 * slot, ((c / KS) - 1) & 1, 520);
             ok = __all_sync(0xffffffffu, here);
             if (!ok) break;
-            const uint8_t* src = stg_p + f * C::F8_TILE;
-            uint8_t* dst = vop_p + slot * C::KV_TILE;
+            const uint8_t* src = stg_p + f * C::STG_TILE;
+            uint8_t* dst = ring_p + slot * C::KV_TILE;
             const int ns = w.slabs_of(j);
-            const bool zero = w.zeroes(j);
+            const bool zero = kv == 1 && w.zeroes(j);
             // staging row rr of slab i holds d = 16 u .. 16 u + 15 in 16-byte unit u ^ (rr & 7); the operand rows hold
             // d in two 64-wide chunks of eight units, unit t at t ^ (row & 7).  Thread r: row r / 8, unit r % 8 of slab i
             const int rr = r >> 3, u = r & 7, cc = u >> 2, t = (u & 3) * 2, sw = rr & 7;
@@ -689,14 +676,15 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               f16_of_e4m3(v.z, o1.x, o1.y);
               f16_of_e4m3(v.w, o1.z, o1.w);
               if (zero && w.hidden(w.slab(j * WP_SLABS + i) * TILE + rr)) o0 = o1 = make_uint4(0, 0, 0, 0);
-              uint8_t* p = dst + i * (2 * TILE * 128) + cc * (TILE * 128) + rr * 128;
+              uint8_t* p = kv == 0 ? dst + cc * (WP_KEYS * 128) + (i * TILE + rr) * 128
+                                   : dst + i * (2 * TILE * 128) + cc * (TILE * 128) + rr * 128;
               *reinterpret_cast<uint4*>(p + ((t ^ sw) << 4)) = o0;
               *reinterpret_cast<uint4*>(p + (((t + 1) ^ sw) << 4)) = o1;
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(vo_full + 8 * slot);
+              mbar_arrive(full + 8 * slot);
               mbar_arrive(sf_empty + 8 * f);
             }
           }
@@ -707,122 +695,203 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::R_SOFTMAX));
     const int X = warp >> 2, r = tid & 127;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
-    uint32_t n_s = 0, no = 0, items = 0;  // S tiles and outputs taken; items
+    const uint32_t s_tile = lane_addr + 128 * X, o_addr = lane_addr + 256 + 128 * X;
+    const float sl = a.scale_log2;
+    uint32_t n_s = 0, no = 0;  // S tiles and outputs taken
     while (ok && next_item(w)) {
-      const uint32_t item = w.j0 < w.j1 ? items++ : 0;
       if (X >= w.nq) continue;
       const int qi = w.i0 + X * QB + r / G;
       const bool valid = r < QB * G && qi < w.i1;
       const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
-      float m = -INFINITY, l = 0.f, sl = a.scale_log2;
-      for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
-        ok = __all_sync(0xffffffffu, wait(s_full + 8 * X, n_s & 1, 600));
-        if (!ok) break;
-        tc_fence_after();
-        if (KV8 && j == w.j0)  // the row's q is scaled by 2^e
-          sl *= __uint_as_float(static_cast<uint32_t>(127 - q_exp[(item & 1) * 256 + X * 128 + r]) << 23);
-        uint32_t sa[2][32], sb[2][32];  // the first 64 keys and the others
-        tmem_ld32(s_addr, sa[0]);
-        tmem_ld32(s_addr + 32, sa[1]);
-        // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
-        const int u0 = j * WP_SLABS, n = w.slabs_of(j);
-        const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
-        const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
-        auto mask = [&](uint32_t (&x)[2][32], int i0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
-            // window (selects, no branches: 128 short branches cost ten times the softmax itself)
-            const int t0 = w.slab(u0 + i0 + i) * TILE;
-            const uint32_t vis = i0 + i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
-            if (__any_sync(0xffffffffu, vis != 0xffffu)) {
-#pragma unroll
-              for (int e = 0; e < TILE; ++e) {
-                uint32_t& v = x[i >> 1][(i & 1) * TILE + e];
-                v = (vis & (1u << e)) ? v : __float_as_uint(-INFINITY);
+      float m = -INFINITY, l = 0.f;
+      if constexpr (KV8) {
+        for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
+          const uint32_t b = n_s & 1, s_addr = s_tile + 64 * b;
+          ok = __all_sync(0xffffffffu, wait(s_full + 16 * X + 8 * b, (n_s >> 1) & 1, 600));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t sv[2][32];
+          tmem_ld32(s_addr, sv[0]);
+          tmem_ld32(s_addr + 32, sv[1]);
+          // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
+          const int u0 = j * WP_SLABS, n = w.slabs_of(j);
+          const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
+          const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
+          tmem_ld_wait();
+          if (edge) {
+  #pragma unroll
+            for (int i = 0; i < WP_SLABS; ++i) {
+              // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
+              // window (selects, no branches: 64 short branches cost ten times the softmax itself)
+              const int t0 = w.slab(u0 + i) * TILE;
+              const uint32_t vis = i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+              if (__any_sync(0xffffffffu, vis != 0xffffu)) {
+  #pragma unroll
+                for (int e = 0; e < TILE; ++e) {
+                  uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
+                  x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
+                }
               }
             }
           }
-        };
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto largest = [&](const uint32_t (&x)[2][32]) {
-#pragma unroll
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  #pragma unroll
           for (int c = 0; c < 2; ++c)
-#pragma unroll
+  #pragma unroll
             for (int e = 0; e < 32; e += 8)
-#pragma unroll
+  #pragma unroll
               for (int t = 0; t < 4; ++t)
-                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(x[c][e + t]), __uint_as_float(x[c][e + t + 4])));
-        };
-        tmem_ld_wait();
-        tmem_ld32(s_addr + 64, sb[0]);  // on their way during the first half's maximum
-        tmem_ld32(s_addr + 96, sb[1]);
-        if (edge) mask(sa, 0);
-        largest(sa);
-        tmem_ld_wait();
-        if (edge) mask(sb, 4);
-        largest(sb);
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        const float m_new = fmaxf(m, mx * sl);
-        // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
-        // l and O so far are rescaled; S(j) is here, so O holds P V(j - 1)
-        if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
-          const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
-          if (j > w.j0) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_addr + 32 * c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(o_addr + 32 * c, o);
+                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(sv[c][e + t]), __uint_as_float(sv[c][e + t + 4])));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float m_new = fmaxf(m, mx * sl);
+          // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
+          // l and O so far are rescaled, once O holds P V(j - 1)
+          if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
+            const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+            if (j > w.j0) {
+              ok = __all_sync(0xffffffffu, wait(o_done + 8 * X, (n_s - 1) & 1, 610));
+              if (!ok) break;
+              tc_fence_after();
+  #pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + 32 * c, o);
+                tmem_ld_wait();
+  #pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(o_addr + 32 * c, o);
+              }
             }
+            l *= alpha;
+            m = m_new;
           }
-          l *= alpha;
-          m = m_new;
-        }
-        // P = 2^(scale s - m), 16-bit, two keys a column, over S of the other keys, which are taken first: E4M3 pools,
-        // whose softmax has fewer registers, read S of the first 64 a second time instead of keeping it; a row that
-        // has seen no key yet keeps m = -inf, and 0 stands in for it
-        const float neg_m = m == -INFINITY ? 0.f : -m;
-        float2 ls[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
-        auto exps = [&](const uint32_t (&x)[32], uint32_t at) {
-          uint32_t pw[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 p = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(sl, sl),
-                            make_float2(neg_m, neg_m));
-            p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
-            ls[e & 3] = add2(ls[e & 3], p);
-            pw[e] = pack2<TP>(p.x, p.y);
+          // P = 2^(scale s - m), 16-bit, two keys a column, over the S just read; a row that has seen no key yet
+          // keeps m = -inf, and 0 stands in for it
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          float2 ls[4];
+  #pragma unroll
+          for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
+  #pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pw[16];
+  #pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 p = fma2(make_float2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])),
+                              make_float2(sl, sl), make_float2(neg_m, neg_m));
+              p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
+              ls[e & 3] = add2(ls[e & 3], p);
+              pw[e] = pack2<TP>(p.x, p.y);
+            }
+            tmem_st16(s_addr + 16 * c, pw);
           }
-          tmem_st16(at, pw);
-        };
-        auto arrive = [&](uint32_t bar) {
+          const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+          l += l2.x + l2.y;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar);
-        };
-        exps(sb[0], s_addr + 96);
-        exps(sb[1], s_addr + 112);
-        if constexpr (KV8) {
+          if (lane == 0) mbar_arrive(p_full + 16 * X + 8 * b);
+        }
+      } else {
+        for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
+          ok = __all_sync(0xffffffffu, wait(s_full + 16 * X, n_s & 1, 600));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s_addr = s_tile;
+          uint32_t sa[2][32], sb[2][32];  // the first 64 keys and the others
           tmem_ld32(s_addr, sa[0]);
           tmem_ld32(s_addr + 32, sa[1]);
+          // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
+          const int u0 = j * WP_SLABS, n = w.slabs_of(j);
+          const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
+          const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
+          auto mask = [&](uint32_t (&x)[2][32], int i0) {
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
+              // window (selects, no branches: 128 short branches cost ten times the softmax itself)
+              const int t0 = w.slab(u0 + i0 + i) * TILE;
+              const uint32_t vis = i0 + i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+              if (__any_sync(0xffffffffu, vis != 0xffffu)) {
+  #pragma unroll
+                for (int e = 0; e < TILE; ++e) {
+                  uint32_t& v = x[i >> 1][(i & 1) * TILE + e];
+                  v = (vis & (1u << e)) ? v : __float_as_uint(-INFINITY);
+                }
+              }
+            }
+          };
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto largest = [&](const uint32_t (&x)[2][32]) {
+  #pragma unroll
+            for (int c = 0; c < 2; ++c)
+  #pragma unroll
+              for (int e = 0; e < 32; e += 8)
+  #pragma unroll
+                for (int t = 0; t < 4; ++t)
+                  mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(x[c][e + t]), __uint_as_float(x[c][e + t + 4])));
+          };
           tmem_ld_wait();
+          tmem_ld32(s_addr + 64, sb[0]);  // on their way during the first half's maximum
+          tmem_ld32(s_addr + 96, sb[1]);
           if (edge) mask(sa, 0);
+          largest(sa);
+          tmem_ld_wait();
+          if (edge) mask(sb, 4);
+          largest(sb);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float m_new = fmaxf(m, mx * sl);
+          // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
+          // l and O so far are rescaled; S(j) is here, so O holds P V(j - 1)
+          if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
+            const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+            if (j > w.j0) {
+  #pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + 32 * c, o);
+                tmem_ld_wait();
+  #pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(o_addr + 32 * c, o);
+              }
+            }
+            l *= alpha;
+            m = m_new;
+          }
+          // P = 2^(scale s - m), 16-bit, two keys a column, over S of the other keys, which are taken first; a
+          // row that has seen no key yet keeps m = -inf, and 0 stands in for it
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          float2 ls[4];
+  #pragma unroll
+          for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
+          auto exps = [&](const uint32_t (&x)[32], uint32_t at) {
+            uint32_t pw[16];
+  #pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 p = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(sl, sl),
+                              make_float2(neg_m, neg_m));
+              p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
+              ls[e & 3] = add2(ls[e & 3], p);
+              pw[e] = pack2<TP>(p.x, p.y);
+            }
+            tmem_st16(at, pw);
+          };
+          auto arrive = [&](uint32_t bar) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+          };
+          exps(sb[0], s_addr + 96);
+          exps(sb[1], s_addr + 112);
+          exps(sa[0], s_addr + 64);
+          arrive(p_most + 8 * X);  // P V may begin with three quarters of the keys
+          exps(sa[1], s_addr + 80);
+          arrive(p_full + 16 * X);
+          const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+          l += l2.x + l2.y;
         }
-        exps(sa[0], s_addr + 64);
-        arrive(p_most + 8 * X);  // P V may begin with three quarters of the keys
-        exps(sa[1], s_addr + 80);
-        arrive(p_full + 8 * X);
-        const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
-        l += l2.x + l2.y;
       }
       if (!ok) break;
       if (w.j0 < w.j1) {
@@ -978,7 +1047,7 @@ int launch_t(Pool& P, DecodeArgs& a, CUtensorMap* maps, const int32_t* q_off, in
   const int64_t keys = std::min(static_cast<int64_t>(a.W) * a.B,
                                 static_cast<int64_t>(a.n_sink) + a.window + std::min<int64_t>(max_q, two) + 2 * TILE);
   int32_t csize = 1;
-  while (csize < 8 && items * csize * 2 <= sms && keys >= 2 * csize * WP_KEYS) csize *= 2;
+  while (csize < 8 && items * csize * 2 <= sms && keys >= 2 * csize * C::KEYS) csize *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(csize > 1 ? items * csize : std::min<int64_t>(items, sms)));
   cfg.blockDim = dim3(C::THREADS);
