@@ -327,7 +327,9 @@ void launch_t(const RotaryArgs& a, cudaStream_t st) {
   const int64_t passes = (rows + rpp - 1) / rpp;
   const int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(passes, cap / a.n_tok)));
   const int groups = static_cast<int>(std::min<int64_t>(a.n_tok, cap / splits));
-  const int tokens = std::min(kTokens, (a.n_tok + groups - 1) / groups), grid = groups * splits;
+  const int64_t share = (static_cast<int64_t>(a.n_tok) + groups - 1) / groups;  // a CTA's tokens, in even tiles
+  const int64_t rounds = (share + kTokens - 1) / kTokens;
+  const int tokens = static_cast<int>((share + rounds - 1) / rounds), grid = groups * splits;
   const size_t smem = static_cast<size_t>(tokens) * a.rot / 2 * sizeof(float2);
   rotary_append_kernel<TA, F8, INTER><<<grid, kRotThreads, smem, st>>>(a, tokens, splits);
 }

@@ -229,6 +229,34 @@ def test_prefill_behind_a_history_longer_than_the_staged_table():
     b.check()
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("e4m3", 128), ("f16", 64)])
+@pytest.mark.parametrize("n", [130, 700])
+def test_prefill_many_sequences(dtype, d, n):
+    """More sequences than the kernel's table has entries, many without a chunk."""
+    chunks = [(i * 7) % 45 if i % 3 else 0 for i in range(n)]
+    lens = [c + (i * 13) % 60 for i, c in enumerate(chunks)]
+    b = Batch(dtype, lens, 31, 3, chunks, H_q=8, H_kv=1, d=d)
+    b.call()
+    b.check(only=set(range(0, n, 19)) | set(range(n - 6, n)))
+
+
+def test_prefill_without_a_chunk_and_two_streams_at_once():
+    b = Batch("bf16", [20, 30], 16, 2, [0, 0], extra_rows=4)
+    b.call(max_q=8)
+    b.check()
+    many = [Batch(t, [600, 900, 33], 200, 4, c, seed=i) for i, (t, c) in
+            enumerate([("bf16", [600, 300, 33]), ("e4m3", [600, 900, 1]), ("bf16", None), ("e4m3", None)])]
+    streams = [torch.cuda.Stream() for _ in many]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, s in zip(many, streams):
+            with torch.cuda.stream(s):
+                x.call()
+    torch.cuda.synchronize()
+    for x in many:
+        x.check()
+
+
 @pytest.mark.parametrize("chunks", [None, [40, 1]])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 96)])
 def test_offsets_past_32_bits(dtype, d, chunks):
