@@ -6,21 +6,30 @@
 //
 // Work: an item is a (sequence, KV head, pair of query blocks); its rows are two M = 128 tiles A and B of (query, head)
 // pairs (row r = query r / G, head r % G).  The keys that some query of the item sees are a list of 16-token slabs --
-// the sinks' slabs, then those from the window's start to the last query -- taken 8 slabs (128 keys) at a time, so that a
-// few sinks cost one slab, not a tile of their own.  Slabs lie in pool blocks of their own: each is one or two TMA boxes.
+// the sinks' slabs, then those from the window's start to the last query -- taken a key tile at a time, so that a few
+// sinks cost one slab, not a tile of their own.  Slabs lie in pool blocks of their own: each is one or two TMA boxes.
+// A window makes items short (1,024 keys are 9 key tiles), so what surrounds them counts: the grid is persistent, and
+// loads, products and softmax of the next item start while this one's rows are written.
 //
-// What bounds it: 4 d flops a (row, key) on the tensor cores, against 128 exponentials a row and key tile on the CUDA
-// cores; the two products of a tile (A) run while the softmax of the other (B) does, so the longer of the two counts.
-// N = 128 keys a product lets its shared-memory reads (A and B operands, 8 KB a K = 16 step) keep up with the
-// multiplies, which N = 64 does not.  A window makes items short (a window of 1,024 is 9 key tiles), so what surrounds them
-// counts: the grid is persistent, and loads, products and softmax of the next item start while this one's rows are written.
+// What bounds it: 4 d flops a (row, key) on the tensor cores, one exponential on the CUDA cores, and the chain between
+// them: Q K, softmax, P V of a key tile follow each other, and only the other row tile fills the gaps.
+//   * 16-bit pools: 128-key tiles (N = 128 products keep their shared-memory reads, 8 KB a K = 16 step, in step with the
+//     multiplies).  S of both tiles and O fill TMEM, so S has one buffer; A and B take turns at the tensor cores, (P V,
+//     Q K) of one, then of the other, and P V starts with three quarters of P.  8 x 512 queries, window 4,096: 400 us,
+//     0.72 of cuBLAS's rate (567 us for the kernel of the calls without a window, given this mask).  Of a key tile's 3,300
+//     cycles the tensor cores work 2,050.  Measured and not kept: 64-key tiles with two S buffers (445 us: the products of
+//     N = 64 wait for shared memory), issuing without turns (530 us: both tiles' softmaxes run at once, then both
+//     products), two threads a row (534 us).
+//   * E4M3 pools: 64-key tiles and two S buffers; codes are converted to binary16 operands by 8 warps (K by 4, V by 4),
+//     which share the multi-function units with the exponentials.  Prompts of 1,500 to 2,500 tokens, window 1,024: 305 us,
+//     0.42 of cuBLAS's 16-bit rate (450 us for the other kernel).  128-key tiles leave too few operand buffers (403 us);
+//     K codes as operands as they are, q as the sum of two E4M3 numbers, cost as much in splitting q (427 us).
 //
 // Roles (warps): 0-3 softmax and epilogue of A, 4-7 of B (a thread a row, its TMEM lane); 8 loads K and V; 9 and 11
-// issue the products of A and of B; 10 loads Q and zeroes V rows that no row sees (0 times whatever lies there must
-// stay 0).  E4M3 pools: 8 loads codes into a staging ring, and warps 12-15 convert them (and q, in place) to binary16.
-// TMEM: S of A and B (128 columns each; P overwrites its last 64), O of A and B from column 256 on.
-// A tile's products are issued by one thread and taken in order, ..., P V(j), Q K(j + 1), ...: S(j + 1) may go over
-// P(j), and its arrival says that O holds P V(j).
+// issue the products of A and of B; 10 looks the items up, loads Q and zeroes V rows that no row sees (0 times whatever
+// lies there must stay 0); E4M3 pools: 12-15 convert K and q of A, 16-19 V and q of B.
+// TMEM: S of A and B (128 columns each; P overwrites scores that have been read), O of A and B from column 256 on.
+// A tile's products are issued by one thread and taken in order, ..., P V(j), Q K(j + 1), ...: Q K may go over P(j).
 //
 // Few items (a short chunk, one sequence) leave SMs idle: there a cluster of up to 8 CTAs takes one item, each a
 // range of its key tiles, and the partial (m, l, O) meet in shared memory.
@@ -49,8 +58,8 @@ struct WpCfg {
   static constexpr int KEYS = KV8 ? 64 : 128, SLABS = KEYS / TILE;  // a key tile
   static constexpr int NCH = D / 64;                      // 64-wide chunks of d (128 bytes, the swizzle's width)
   static constexpr int Q_TILE = 128 * D * 2;              // one Q tile
-  static constexpr int KV_TILE = KEYS * D * 2;         // one K or V tile as an operand (16-bit)
-  static constexpr int STG_TILE = KEYS * D;            // one K or V tile of E4M3 codes
+  static constexpr int KV_TILE = KEYS * D * 2;            // one K or V tile as an operand (16-bit)
+  static constexpr int STG_TILE = KEYS * D;               // one K or V tile of E4M3 codes
   static constexpr int KS = KV8 ? 6 : (D == 64 ? 8 : 5);  // operand ring: K and V tiles in turn
   static constexpr int FS = KV8 ? 8 : 0;                  // staging ring
   static constexpr int BARS = 3 + 3 * KS + 2 * 4 + 5 * 2 + 4 + 2 * FS;
@@ -409,9 +418,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       // ------------------------------------------------------------ the products of tile X (9: A, 11: B)
       // The whole warp walks the items, so that descriptors stay warp-uniform, and one elected lane issues: a
       // divergent thread on its own needs some 140 cycles a product to bring its operands into uniform registers.
-      // A and B take turns, (P V, Q K) of one, then of the other, so that S of A arrives while B's products run and the
-      // two softmaxes stay half a period apart; issued side by side, the products of both end together, and then both
-      // softmaxes run while the tensor cores wait.  A tile without rows (nq = 1) has its turns all the same.
+      // 16-bit pools: A and B take turns, so that S of A arrives while B's products run and the two softmaxes stay half a
+      // period apart.  E4M3 pools: S has two buffers, so that Q K of the next key tile runs while this one's softmax does.
+      // A tile without rows (nq = 1) has its turns, and its part in the operand ring, all the same.
       // (the broadcasts from lane 0 are what tells the compiler that a value is the same in all lanes)
       auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
       const int X = uni(warp == 9 ? 0 : 1);
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
             const uint32_t b = ns_ & 1;
             if (elect_one()) {
               if (live) {
-  #pragma unroll
+#pragma unroll
                 for (int k = 0; k < D / 16; ++k)  // 64-wide chunk; 16 elements along its 128-byte row
                   umma_ss(s_tm + 64 * b, q_desc + ((k >> 2) * 16384 + (k & 3) * 32) / 16,
                           kd + ((k >> 2) * (WP_KEYS * 128) + (k & 3) * 32) / 16, idesc_s, k > 0);
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
             const int n = min(WP_SLABS, nslab - i * WP_SLABS);
             if (elect_one()) {
               if (live) {
-  #pragma unroll
+#pragma unroll
                 for (int k = 0; k < WP_SLABS; ++k)
                   if (k < n)
                     umma_ts(o_tm, s_tm + 64 * b + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
@@ -496,8 +505,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           }
           c += 2 * nt;
           if (!live) ns_ -= nt, np -= nt;  // no S or P of this tile
-        } else
-        for (int i = -1; i < nt && ok; ++i) {  // P V of the item's i-th key tile, then Q K of the next
+        }
+        for (int i = -1; !KV8 && i < nt && ok; ++i) {  // P V of the item's i-th key tile, then Q K of the next
           // everything is waited for before the turn: within it the products follow each other without a gap
           const bool has_pv = i >= 0, has_qk = i + 1 < nt;
           const uint32_t vs = c % KS, ks = (c + has_pv) % KS;
@@ -523,21 +532,18 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
             if (k < nv)
               umma_ts(o_tm, s_tm + 64 + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
           };
-          if (live && has_pv) {  // three quarters of P, then (it came meanwhile) the rest
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < WP_SLABS; ++k)
-                if (k < 2 || k >= 4) pv(k);
-            }
-            __syncwarp();
-            ok = wait_all(p_full + 16 * X, np++ & 1, 250);
-            if (!ok) break;
-            tc_fence_after();
-          }
+          bool came = true;
           if (elect_one()) {
             if (live) {
+              if (has_pv) {  // three quarters of P, then (it came meanwhile) the rest
 #pragma unroll
-              for (int k = 2; k < 4; ++k) pv(k);
+                for (int k = 0; k < WP_SLABS; ++k)
+                  if (k < 2 || k >= 4) pv(k);
+                came = wait(p_full + 16 * X, np & 1, 250);
+                tc_fence_after();
+#pragma unroll
+                for (int k = 2; k < 4; ++k) pv(k);
+              }
               if (has_qk) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {  // 64-wide chunk; 16 elements along its 128-byte row
@@ -562,7 +568,8 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
               if (i + 2 == nt) mbar_arrive(u_q_empty);
             }
           }
-          __syncwarp();
+          np += live && has_pv;
+          ok = __all_sync(0xffffffffu, came);
         }
       }
       if (*abort_flag) {
@@ -704,194 +711,132 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       const bool valid = r < QB * G && qi < w.i1;
       const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
-      float m = -INFINITY, l = 0.f;
-      if constexpr (KV8) {
-        for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
-          const uint32_t b = n_s & 1, s_addr = s_tile + 64 * b;
-          ok = __all_sync(0xffffffffu, wait(s_full + 16 * X + 8 * b, (n_s >> 1) & 1, 600));
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t sv[2][32];
-          tmem_ld32(s_addr, sv[0]);
-          tmem_ld32(s_addr + 32, sv[1]);
-          // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
-          const int u0 = j * WP_SLABS, n = w.slabs_of(j);
-          const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
-          const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
-          tmem_ld_wait();
-          if (edge) {
-  #pragma unroll
-            for (int i = 0; i < WP_SLABS; ++i) {
-              // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
-              // window (selects, no branches: 64 short branches cost ten times the softmax itself)
-              const int t0 = w.slab(u0 + i) * TILE;
-              const uint32_t vis = i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
-              if (__any_sync(0xffffffffu, vis != 0xffffu)) {
-  #pragma unroll
-                for (int e = 0; e < TILE; ++e) {
-                  uint32_t& x = sv[i >> 1][(i & 1) * TILE + e];
-                  x = (vis & (1u << e)) ? x : __float_as_uint(-INFINITY);
-                }
+      float m = -INFINITY, l = 0.f, mx;
+      float2 ls[4];
+      for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
+        const uint32_t b = KV8 ? n_s & 1 : 0, s_addr = s_tile + 64 * b;
+        ok = __all_sync(0xffffffffu, wait(s_full + 16 * X + 8 * b, (KV8 ? n_s >> 1 : n_s) & 1, 600));
+        if (!ok) break;
+        tc_fence_after();
+        // the tile's last 64 keys and, 16-bit pools, its first 64
+        uint32_t sb[2][32], sa[KV8 ? 1 : 2][32];
+        constexpr int B0 = KV8 ? 0 : 64;
+        tmem_ld32(s_addr + B0, sb[0]);
+        tmem_ld32(s_addr + B0 + 32, sb[1]);
+        // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
+        const int u0 = j * WP_SLABS, n = w.slabs_of(j);
+        const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
+        const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
+        auto mask = [&](uint32_t (&x)[2][32], int i0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
+            // window (selects, no branches: 128 short branches cost ten times the softmax itself)
+            const int t0 = w.slab(u0 + i0 + i) * TILE;
+            const uint32_t vis = i0 + i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
+            if (__any_sync(0xffffffffu, vis != 0xffffu)) {
+#pragma unroll
+              for (int e = 0; e < TILE; ++e) {
+                uint32_t& v = x[i >> 1][(i & 1) * TILE + e];
+                v = (vis & (1u << e)) ? v : __float_as_uint(-INFINITY);
               }
             }
           }
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  #pragma unroll
+        };
+        auto largest = [&](const uint32_t (&x)[2][32], float from) {
+          float mx4[4] = {from, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
           for (int c = 0; c < 2; ++c)
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 32; e += 8)
-  #pragma unroll
+#pragma unroll
               for (int t = 0; t < 4; ++t)
-                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(sv[c][e + t]), __uint_as_float(sv[c][e + t + 4])));
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const float m_new = fmaxf(m, mx * sl);
-          // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
-          // l and O so far are rescaled, once O holds P V(j - 1)
-          if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
-            const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
-            if (j > w.j0) {
-              ok = __all_sync(0xffffffffu, wait(o_done + 8 * X, (n_s - 1) & 1, 610));
-              if (!ok) break;
-              tc_fence_after();
-  #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_addr + 32 * c, o);
-                tmem_ld_wait();
-  #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st32(o_addr + 32 * c, o);
-              }
-            }
-            l *= alpha;
-            m = m_new;
-          }
-          // P = 2^(scale s - m), 16-bit, two keys a column, over the S just read; a row that has seen no key yet
-          // keeps m = -inf, and 0 stands in for it
+                mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(x[c][e + t]), __uint_as_float(x[c][e + t + 4])));
+          return fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        };
+        // P = 2^(scale s - m), 16-bit, two keys a column, over scores that have been read; a row that has seen no key
+        // yet keeps m = -inf, and 0 stands in for it
+        auto exps = [&](const uint32_t (&x)[32], uint32_t at) {
           const float neg_m = m == -INFINITY ? 0.f : -m;
-          float2 ls[4];
-  #pragma unroll
-          for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
-  #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pw[16];
-  #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 p = fma2(make_float2(__uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1])),
-                              make_float2(sl, sl), make_float2(neg_m, neg_m));
-              p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
-              ls[e & 3] = add2(ls[e & 3], p);
-              pw[e] = pack2<TP>(p.x, p.y);
-            }
-            tmem_st16(s_addr + 16 * c, pw);
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 p = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(sl, sl),
+                            make_float2(neg_m, neg_m));
+            p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
+            ls[e & 3] = add2(ls[e & 3], p);
+            pw[e] = pack2<TP>(p.x, p.y);
           }
-          const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
-          l += l2.x + l2.y;
+          tmem_st16(at, pw);
+        };
+        auto arrive = [&](uint32_t bar) {
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + 16 * X + 8 * b);
-        }
-      } else {
-        for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
-          ok = __all_sync(0xffffffffu, wait(s_full + 16 * X, n_s & 1, 600));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t s_addr = s_tile;
-          uint32_t sa[2][32], sb[2][32];  // the first 64 keys and the others
+          if (lane == 0) mbar_arrive(bar);
+        };
+        constexpr int P0 = KV8 ? 0 : 64;  // P's columns in S (16-bit pools: keys 64 .. are in the last 32 of them)
+        auto first_exps = [&] {
+          exps(sb[0], s_addr + P0 + (KV8 ? 0 : 32));
+          exps(sb[1], s_addr + P0 + (KV8 ? 16 : 48));
+        };
+        // The reference maximum of a row moves only when the row's grows by more than 2^8 (until then P and l share the
+        // old one), which is rare after the first tile.  E4M3 pools take the exponentials with the old one while the new
+        // maximum is found, and once more if it moves (305 -> 300 us; with 16-bit pools' longer turns it costs 9 %).
+        const bool early = KV8 && !__any_sync(0xffffffffu, m == -INFINITY);
+        if (early)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
+        tmem_ld_wait();
+        if constexpr (!KV8) {
           tmem_ld32(s_addr, sa[0]);
           tmem_ld32(s_addr + 32, sa[1]);
-          // mask only tiles that hold a key hidden from a row of the warp (or columns that were not computed)
-          const int u0 = j * WP_SLABS, n = w.slabs_of(j);
-          const int t_first = w.slab(u0) * TILE, t_last = w.slab(u0 + n - 1) * TILE + TILE - 1;
-          const bool edge = __any_sync(0xffffffffu, n < WP_SLABS || t_last > lim || t_first < low);
-          auto mask = [&](uint32_t (&x)[2][32], int i0) {
-  #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // the slab's visible elements as bits: up to the row's last key, less those between its sinks and its
-              // window (selects, no branches: 128 short branches cost ten times the softmax itself)
-              const int t0 = w.slab(u0 + i0 + i) * TILE;
-              const uint32_t vis = i0 + i < n ? below(lim + 1 - t0) & ~(below(low - t0) & ~below(a.n_sink - t0)) : 0u;
-              if (__any_sync(0xffffffffu, vis != 0xffffu)) {
-  #pragma unroll
-                for (int e = 0; e < TILE; ++e) {
-                  uint32_t& v = x[i >> 1][(i & 1) * TILE + e];
-                  v = (vis & (1u << e)) ? v : __float_as_uint(-INFINITY);
-                }
-              }
-            }
-          };
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto largest = [&](const uint32_t (&x)[2][32]) {
-  #pragma unroll
-            for (int c = 0; c < 2; ++c)
-  #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-  #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                  mx4[t] = fmaxf(mx4[t], fmaxf(__uint_as_float(x[c][e + t]), __uint_as_float(x[c][e + t + 4])));
-          };
-          tmem_ld_wait();
-          tmem_ld32(s_addr + 64, sb[0]);  // on their way during the first half's maximum
-          tmem_ld32(s_addr + 96, sb[1]);
-          if (edge) mask(sa, 0);
-          largest(sa);
-          tmem_ld_wait();
-          if (edge) mask(sb, 4);
-          largest(sb);
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const float m_new = fmaxf(m, mx * sl);
-          // the reference maximum moves when a row's grows by more than 2^8 (until then P and l share the old one):
-          // l and O so far are rescaled; S(j) is here, so O holds P V(j - 1)
-          if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
-            const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
-            if (j > w.j0) {
-  #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_addr + 32 * c, o);
-                tmem_ld_wait();
-  #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st32(o_addr + 32 * c, o);
-              }
-            }
-            l *= alpha;
-            m = m_new;
-          }
-          // P = 2^(scale s - m), 16-bit, two keys a column, over S of the other keys, which are taken first; a
-          // row that has seen no key yet keeps m = -inf, and 0 stands in for it
-          const float neg_m = m == -INFINITY ? 0.f : -m;
-          float2 ls[4];
-  #pragma unroll
-          for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
-          auto exps = [&](const uint32_t (&x)[32], uint32_t at) {
-            uint32_t pw[16];
-  #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 p = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(sl, sl),
-                              make_float2(neg_m, neg_m));
-              p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
-              ls[e & 3] = add2(ls[e & 3], p);
-              pw[e] = pack2<TP>(p.x, p.y);
-            }
-            tmem_st16(at, pw);
-          };
-          auto arrive = [&](uint32_t bar) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-          };
-          exps(sb[0], s_addr + 96);
-          exps(sb[1], s_addr + 112);
-          exps(sa[0], s_addr + 64);
-          arrive(p_most + 8 * X);  // P V may begin with three quarters of the keys
-          exps(sa[1], s_addr + 80);
-          arrive(p_full + 16 * X);
-          const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
-          l += l2.x + l2.y;
         }
+        if (edge) mask(sb, KV8 ? 0 : 4);
+        if (early) first_exps();
+        mx = largest(sb, -INFINITY);
+        if constexpr (!KV8) {
+          tmem_ld_wait();
+          if (edge) mask(sa, 0);
+          if constexpr (!KV8) mx = largest(sa, mx);
+        }
+        const float m_new = fmaxf(m, mx * sl);
+        const bool moves = __any_sync(0xffffffffu, m_new > m + 8.f);
+        if (moves) {
+          // l and O so far are rescaled, once O holds P V(j - 1) (16-bit pools: S(j) is here, so it does)
+          const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m - m_new);
+          if (j > w.j0) {
+            if constexpr (KV8) {
+              ok = __all_sync(0xffffffffu, wait(o_done + 8 * X, (n_s - 1) & 1, 610));
+              if (!ok) break;
+              tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(o_addr + 32 * c, o);
+            }
+          }
+          l *= alpha;
+          m = m_new;
+        }
+        if (!early || moves) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
+          first_exps();
+          if constexpr (!KV8) exps(sa[0], s_addr + P0);
+        }
+        if constexpr (!KV8) {
+          arrive(p_most + 8 * X);  // P V may begin with three quarters of the keys
+          exps(sa[1], s_addr + P0 + 16);
+        }
+        arrive(p_full + 16 * X + 8 * b);
+        const float2 l2 = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+        l += l2.x + l2.y;
       }
       if (!ok) break;
       if (w.j0 < w.j1) {
