@@ -441,11 +441,15 @@ int pkv_prefill_attention(const pkv_pool* pool, int32_t layer, const void* q, co
  * Keys that no query of the call sees have no effect whatever their bytes, and the blocks that
  * hold none of the others are neither read nor looked up: their table entries may hold anything.
  * pkv_decode_attention_window: one query per sequence, at position len_s - 1.  Arguments, types,
- *   workspace, kernels and limits as for pkv_decode_attention; batches lay out only the 16-token
- *   tiles that hold a visible key, so every warp reads the same number of visible bytes.
- * pkv_prefill_attention_window: the queries of a chunk, each with its own window.  Arguments, types,
- *   kernels and limits as for pkv_prefill_attention; rows of q and out past q_offsets[n_seq] are
- *   neither read nor written.  A key that one query of the chunk sees and another does not must
+ *   workspace and limits as for pkv_decode_attention.  On tensor cores the persistent kernel of that
+ *   call, over the 16-token tiles that hold a visible key; batches of at most as many (sequence,
+ *   KV head) pairs as SMs a cluster of 1 to 8 CTAs per pair instead (which leaves the workspace
+ *   alone).
+ * pkv_prefill_attention_window: the queries of a chunk, each with its own window.  Arguments, types
+ *   and limits as for pkv_prefill_attention; bf16/f16 pools with d_head 64 or 128 and FP8 pools with
+ *   d_head 128, B a multiple of 16, run on tcgen05 tensor cores (few rows: a cluster of CTAs per
+ *   block of rows), other geometries on CUDA cores (at most 16 query heads per KV head, 8 with
+ *   d_head > 128).  Rows of q and out past q_offsets[n_seq] are neither read nor written.  A key that one query of the chunk sees and another does not must
  *   be finite, as in pkv_prefill_attention: 0 times its value reaches rows of the same tile.
  * scale must be finite and > 0.  The calls may be captured into a graph and replayed. */
 int pkv_decode_attention_window(const pkv_pool* pool, int32_t layer, const void* q, const void* k_pool,
