@@ -570,7 +570,7 @@ def pkv_append_kv_rotary(pool: Pool, layer: int, rotary: Rotary, q, k_new, v_new
     dtype, H_q, H_kv, d = pool._dims
     act, i32 = pool._act_types or pool._resolve_types(), _TORCH_TYPES["i32"][1]
     n = slot_mapping.numel()
-    if positions.numel() != rotary.n_axes * n or (rotary.n_axes > 1 and positions.dim() != 2):
+    if positions.shape != (rotary.n_axes, n) and (rotary.n_axes > 1 or positions.shape != (n,)):
         raise ValueError(f"positions has shape {tuple(positions.shape)}, not {(rotary.n_axes, n)}")
     if rotary.inv_freq.get_device() != dev:
         raise ValueError(f"inv_freq is on cuda:{rotary.inv_freq.get_device()}, the current device is cuda:{dev}")

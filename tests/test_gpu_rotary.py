@@ -225,6 +225,10 @@ def test_refusals_of_the_binding():
     ]:
         with pytest.raises(error, match=text):
             c.call(**kw)
+    t = Case("bf16", n=12, d=64, axes=HALVES_3)
+    for wrong in (t.positions.t().contiguous(), t.positions.reshape(-1)):  # as many positions, but in another order
+        with pytest.raises(ValueError, match="positions"):
+            t.call(positions=wrong)
     with pytest.raises(ValueError, match="entries"):
         pkv.Rotary(torch.ones(129, device="cuda"))
     with pytest.raises(ValueError, match="axes"):

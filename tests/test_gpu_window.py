@@ -154,6 +154,51 @@ def test_decode_geometries(kw, window, n_sink):
     b.check()
 
 
+# more (sequence, KV head) pairs than SMs: the persistent kernel, whose warps cut pairs anywhere
+MANY = [(i * 131) % 2100 for i in range(60)] + [0, 1, 16, 17]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype="bf16", H_q=64, H_kv=8), dict(dtype="f16", H_q=8, H_kv=8, d=64, B=32), dict(dtype="f16", H_q=64, H_kv=4, d=64),
+    dict(dtype="bf16", H_q=96, H_kv=8, B=48), dict(dtype="e4m3", H_q=28, H_kv=4, B=64), dict(dtype="e4m3", H_q=128, H_kv=8),
+], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (50, 4), (333, 0), (129, 200), (7, 40), (2**31 - 1, 5)])
+def test_decode_many_pairs(kw, window, n_sink):
+    b = Batch(lens=MANY, window=window, n_sink=n_sink, **kw)
+    b.call()
+    b.check()
+
+
+def test_decode_many_pairs_replayed():
+    """The persistent kernel counts the parts of a pair anew at every replay."""
+    a = Batch("bf16", MANY, 900, 4, H_q=64, H_kv=8)
+    b = Batch("e4m3", MANY[::-1], 500, 0, H_q=32, H_kv=4, seed=1)
+    ws = a.ws if a.ws.numel() >= b.ws.numel() else b.ws
+    graphs = []
+    for x in (a, b):
+        x.call(ws=ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            x.call(ws=ws)
+    for turn in range(3):
+        for x, graph in zip((a, b), graphs):
+            x.q.copy_(torch.randn_like(x.q))
+            x.out.fill_(math.nan)
+            graph.replay()
+            x.check()
+    plain = torch.cuda.CUDAGraph()  # the call without a window, too
+    whole = Batch("bf16", MANY, 4096, 0, H_q=64, H_kv=8)
+    pkv.pkv_decode_attention(whole.pool, 0, whole.q, whole.kp, whole.vp, whole.tables, whole.lens_d, whole.scale, whole.out, whole.ws)
+    with torch.cuda.graph(plain):
+        pkv.pkv_decode_attention(whole.pool, 0, whole.q, whole.kp, whole.vp, whole.tables, whole.lens_d, whole.scale, whole.out,
+                                 whole.ws)
+    for _ in range(3):
+        whole.q.copy_(torch.randn_like(whole.q))
+        whole.out.fill_(math.nan)
+        plain.replay()
+        whole.check()
+
+
 def test_decode_one_long_sequence_over_the_whole_grid():
     b = Batch("bf16", [70001], 20011, 5, H_q=64, H_kv=8)
     b.call()
@@ -203,7 +248,8 @@ def test_prefill_windows(dtype, window, n_sink, lens, chunks):
 @pytest.mark.parametrize("kw", [
     dict(dtype="f16", H_q=64, H_kv=8), dict(dtype="bf16", H_q=4, H_kv=4, B=32), dict(dtype="bf16", H_q=6, H_kv=2, B=64),
     dict(dtype="f16", H_q=12, H_kv=1), dict(dtype="bf16", H_q=64, H_kv=1), dict(dtype="e4m3", H_q=32, H_kv=2, B=128),
-    dict(dtype="e4m3", H_q=5, H_kv=5), dict(dtype="bf16", H_q=16, H_kv=2, L=2, layer=1),
+    dict(dtype="e4m3", H_q=5, H_kv=5), dict(dtype="bf16", H_q=128, H_kv=1), dict(dtype="e4m3", H_q=100, H_kv=1),
+    dict(dtype="f16", H_q=66, H_kv=1, d=64), dict(dtype="bf16", H_q=16, H_kv=2, L=2, layer=1),
     # mma.sync (d_head 64)
     dict(dtype="bf16", H_q=16, H_kv=2, d=64), dict(dtype="f16", H_q=3, H_kv=3, d=64, B=32), dict(dtype="f16", H_q=7, H_kv=1, d=64),
     # CUDA cores
