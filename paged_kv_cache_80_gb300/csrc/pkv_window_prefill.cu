@@ -15,8 +15,8 @@
 // them: Q K, softmax, P V of a key tile follow each other, and only the other row tile fills the gaps.
 //   * 16-bit pools: 128-key tiles (N = 128 products keep their shared-memory reads, 8 KB a K = 16 step, in step with the
 //     multiplies).  S of both tiles and O fill TMEM, so S has one buffer; A and B take turns at the tensor cores, (P V,
-//     Q K) of one, then of the other, and P V starts with three quarters of P.  8 x 512 queries, window 4,096: 400 us,
-//     0.72 of cuBLAS's rate (567 us for the kernel of the calls without a window, given this mask).  Of a key tile's 3,300
+//     Q K) of one, then of the other, and P V starts with half of P.  8 x 512 queries, window 4,096: 392 us,
+//     0.73 of cuBLAS's rate (567 us for the kernel of the calls without a window, given this mask).  Of a key tile's 3,300
 //     cycles the tensor cores work 2,050.  Measured and not kept: 64-key tiles with two S buffers (445 us: the products of
 //     N = 64 wait for shared memory), issuing without turns (530 us: both tiles' softmaxes run at once, then both
 //     products), two threads a row (534 us).
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   uint8_t* bar_p = base + C::DATA;
   const uint32_t q_full = smem_u32(bar_p), q_ready = q_full + 8, q_empty = q_full + 16;
   const uint32_t full = q_full + 24, empty = full + 8 * KS, land = empty + 8 * KS;  // operand ring; V tiles to be zeroed
-  // per tile A, B: S and P (E4M3: of an even and of an odd key tile); three quarters of P, P V done; the item's O done;
+  // per tile A, B: S and P (E4M3: of an even and of an odd key tile); half of P, P V done; the item's O done;
   // the turn to issue; after an abort
   const uint32_t s_full = land + 8 * KS, p_full = s_full + 32, p_most = p_full + 32, o_done = p_most + 16;
   const uint32_t o_full = o_done + 16, turn = o_full + 16, drain = turn + 16;
@@ -527,22 +527,23 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           const int nv = has_pv ? min(WP_SLABS, nslab - i * WP_SLABS) : 0;
           const uint32_t idesc_s =
               umma_idesc_f16(BF16, 128, has_qk ? min(WP_SLABS, nslab - (i + 1) * WP_SLABS) * TILE : TILE, false);
-          // P of keys 0 .. 31 and 64 .. 127 comes first (slabs 0, 1, 4 .. 7; slab 0 is always there)
+          // P of keys 64 .. 127 comes first (slabs 4 .. 7, where the tile has them)
+          const int k0 = nv > 4 ? 4 : 0;
           auto pv = [&](int k) {
             if (k < nv)
-              umma_ts(o_tm, s_tm + 64 + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+              umma_ts(o_tm, s_tm + 64 + 8 * k, vd + k * (C::NCH * TILE * 128 / 16), idesc_o, i > 0 || k != k0 ? 1u : 0u);
           };
           bool came = true;
           if (elect_one()) {
             if (live) {
-              if (has_pv) {  // three quarters of P, then (it came meanwhile) the rest
+              if (has_pv) {  // half of P, then (it comes meanwhile) the rest
 #pragma unroll
                 for (int k = 0; k < WP_SLABS; ++k)
-                  if (k < 2 || k >= 4) pv(k);
+                  if (k >= 4) pv(k);
                 came = wait(p_full + 16 * X, np & 1, 250);
                 tc_fence_after();
 #pragma unroll
-                for (int k = 2; k < 4; ++k) pv(k);
+                for (int k = 0; k < 4; ++k) pv(k);
               }
               if (has_qk) {
 #pragma unroll
@@ -828,10 +829,10 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
 #pragma unroll
           for (int t = 0; t < 4; ++t) ls[t] = make_float2(0.f, 0.f);
           first_exps();
-          if constexpr (!KV8) exps(sa[0], s_addr + P0);
         }
         if constexpr (!KV8) {
-          arrive(p_most + 8 * X);  // P V may begin with three quarters of the keys
+          arrive(p_most + 8 * X);  // P V may begin with half of the keys
+          exps(sa[0], s_addr + P0);
           exps(sa[1], s_addr + P0 + 16);
         }
         arrive(p_full + 16 * X + 8 * b);
