@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
   const int64_t step = csize > 1 ? n_items : gridDim.x;  // a cluster takes one item
   const int64_t begin = csize > 1 ? blockIdx.x / csize : blockIdx.x;
 
-  // item idx; false for one without work.  `record` reports bad values.
+  // item idx (called by a whole warp); false for one without work.  `record` reports bad values.
   auto get = [&](int64_t idx, Item& w, bool record) __attribute__((always_inline)) -> bool {
     int lo = 0, hi = groups - 1;
     while (lo < hi) {
@@ -274,10 +274,29 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
     }
     int64_t r = idx - static_cast<int64_t>(pre[lo]) * a.H_kv;
     w.s = lo * per;
-    int nb = pairs_of(w.s, false);
-    while (r >= static_cast<int64_t>(nb) * a.H_kv && w.s + 1 < a.n_seq) {
-      r -= static_cast<int64_t>(nb) * a.H_kv;
-      nb = pairs_of(++w.s, false);
+    int nb = 0;
+    if (per == 1) {
+      nb = pairs_of(w.s, false);
+    } else {  // among the group's sequences, 32 at a time
+      const int end = min(a.n_seq, w.s + per);
+      for (; w.s < end && nb == 0; w.s += 32) {
+        const int n = w.s + lane < end ? pairs_of(w.s + lane, false) : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, static_cast<int64_t>(incl) * a.H_kv > r);
+        const int at = past ? __ffs(past) - 1 : 31;  // the lane whose sequence holds the item
+        if (past) {
+          nb = __shfl_sync(0xffffffffu, n, at);
+          r -= static_cast<int64_t>(__shfl_sync(0xffffffffu, incl, at) - nb) * a.H_kv;
+          w.s += at;
+          break;
+        }
+        r -= static_cast<int64_t>(__shfl_sync(0xffffffffu, incl, 31)) * a.H_kv;
+      }
     }
     if (nb == 0 || r < 0 || r >= static_cast<int64_t>(nb) * a.H_kv) return false;
     w.g = static_cast<int>(r) / nb;
