@@ -449,8 +449,9 @@ int pkv_prefill_attention(const pkv_pool* pool, int32_t layer, const void* q, co
  *   and limits as for pkv_prefill_attention; bf16/f16 pools with d_head 64 or 128 and FP8 pools with
  *   d_head 128, B a multiple of 16, run on tcgen05 tensor cores (few rows: a cluster of CTAs per
  *   block of rows), other geometries on CUDA cores (at most 16 query heads per KV head, 8 with
- *   d_head > 128).  Rows of q and out past q_offsets[n_seq] are neither read nor written.  A key that one query of the chunk sees and another does not must
- *   be finite, as in pkv_prefill_attention: 0 times its value reaches rows of the same tile.
+ *   d_head > 128).  Rows of q past q_offsets[n_seq] have no effect, rows of out there are not
+ *   written.  A key that one query of the chunk sees and another does not must be finite, as in
+ *   pkv_prefill_attention: 0 times its value reaches rows of the same tile.
  * scale must be finite and > 0.  The calls may be captured into a graph and replayed. */
 int pkv_decode_attention_window(const pkv_pool* pool, int32_t layer, const void* q, const void* k_pool,
                                 const void* v_pool, const int32_t* block_tables, int32_t W, const int32_t* seq_lens,

@@ -731,7 +731,9 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
       const bool valid = r < QB * G && qi < w.i1;
       const int lim = valid ? w.P + qi : w.nkeys - 1;                  // last visible key
       const int low = visible_at(a.window, a.n_sink, lim).lo;          // from here on visible, before only the sinks
-      float m = -INFINITY, l = 0.f, mx;
+      // a tile's other rows (past the chunk, past QB G) hold whatever lies there: their m stays as it is, so that no
+      // vote of the warp, and with it no rounding of a row, depends on them
+      float m = valid ? -INFINITY : 0.f, l = 0.f, mx;
       float2 ls[4];
       for (int j = w.j0; j < w.j1 && ok; ++j, ++n_s) {
         const uint32_t b = KV8 ? n_s & 1 : 0, s_addr = s_tile + 64 * b;
@@ -820,7 +822,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
           if (edge) mask(sa, 0);
           if constexpr (!KV8) mx = largest(sa, mx);
         }
-        const float m_new = fmaxf(m, mx * sl);
+        const float m_new = valid ? fmaxf(m, mx * sl) : m;
         const bool moves = __any_sync(0xffffffffu, m_new > m + 8.f);
         if (moves) {
           // l and O so far are rescaled, once O holds P V(j - 1) (16-bit pools: S(j) is here, so it does)

@@ -330,6 +330,27 @@ def test_a_wide_window_is_the_whole_sequence(dtype):
     p.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H_q,H_kv", [(3, 1), (24, 1), (80, 2)])  # 128 is no multiple of the queries of a KV head
+def test_prefill_rows_depend_on_their_own_sequence_alone(dtype, H_q, H_kv):
+    """The same bits whatever the next sequence's queries, the rows behind the last one and the calls before."""
+    b = Batch(dtype, [700, 300, 90], 200, 4, [33, 130, 7], H_q=H_q, H_kv=H_kv, extra_rows=9)
+    b.call()
+    b.check()
+    first = b.out.clone()
+    rows = slice(b.offs[1], b.offs[2])
+    others = [i for i in range(b.offs[-1]) if not b.offs[1] <= i < b.offs[2]]
+    q = b.q.clone()
+    for k in (100.0, 0.0, 30.0):
+        b.q[others] = q[others] * k
+        b.q[b.offs[-1]:] = math.nan if k else 1000.0
+        b.call()
+        assert torch.equal(b.out[rows], first[rows]), k
+    b.q.copy_(q)
+    b.call()
+    assert torch.equal(b.out[:b.offs[-1]], first[:b.offs[-1]])
+
+
 def test_replayed_graphs_that_share_a_workspace():
     """Every replay counts its split pairs anew: two graphs, replayed in turn with new lengths, queries and workspace bytes."""
     a = Batch("bf16", [3000, 17, 800], 900, 4, H_q=64, H_kv=8)
