@@ -569,6 +569,7 @@ def pkv_append_kv_rotary(pool: Pool, layer: int, rotary: Rotary, q, k_new, v_new
     dev = _current_device()
     dtype, H_q, H_kv, d = pool._dims
     act, i32 = pool._act_types or pool._resolve_types(), _TORCH_TYPES["i32"][1]
+    pp, sp = _dev_as(positions, "positions", i32, dev), _dev_as(slot_mapping, "slot_mapping", i32, dev)
     n = slot_mapping.numel()
     if positions.shape != (rotary.n_axes, n) and (rotary.n_axes > 1 or positions.shape != (n,)):
         raise ValueError(f"positions has shape {tuple(positions.shape)}, not {(rotary.n_axes, n)}")
@@ -584,9 +585,7 @@ def pkv_append_kv_rotary(pool: Pool, layer: int, rotary: Rotary, q, k_new, v_new
     kn, ks = _rows(k_new, "k_new", shape, act, dev)
     vn, vs = _rows(v_new, "v_new", shape, act, dev)
     kp, vp = _pools(pool, k_pool, v_pool, dev)
-    rc = L.pkv_append_kv_rotary(pool.handle, layer, rotary._addr, qp, qs, kn, ks, vn, vs,
-                                _dev_as(positions, "positions", i32, dev),
-                                _dev_as(slot_mapping, "slot_mapping", i32, dev), n, op, os_, kp, vp,
+    rc = L.pkv_append_kv_rotary(pool.handle, layer, rotary._addr, qp, qs, kn, ks, vn, vs, pp, sp, n, op, os_, kp, vp,
                                 _stream_on(stream, dev))
     if rc:
         _check(rc, "pkv_append_kv_rotary")
@@ -839,21 +838,29 @@ def pkv_prefill_attention(pool: PoolLike, layer: int, q, q_offsets, max_q: int, 
                                       float(scale), _dev(out, "out"), _stream(stream)), "pkv_prefill_attention")
 
 
-def _attention_args(pool: Pool, q, k_pool, v_pool, block_tables, seq_lens, out, rows: int, device: int):
+_I32_MAX = 2**31 - 1  # a window or sinks beyond it mean what it means: more than every length
+
+
+def _attention_args(pool: Pool, q, k_pool, v_pool, block_tables, seq_lens, out, prefill: bool, device: int):
     """Pointers of a windowed attention call's tensors, their types, shapes and device checked:
-    (q, k_pool, v_pool, block_tables, W, seq_lens, n_seq, out)."""
+    (q, rows of q, k_pool, v_pool, block_tables, W, seq_lens, n_seq, out)."""
     dtype, H_q, H_kv, d = pool._dims
     act = pool._act_types or pool._resolve_types()
     i32 = _TORCH_TYPES["i32"][1]
-    shape = (rows, H_q, d)
-    qp, op = _dev_as(q, "q", act, device, shape), _dev_as(out, "out", act, device, shape)
-    kp, vp = _pools(pool, k_pool, v_pool, device)
     tp, lp = _dev_as(block_tables, "block_tables", i32, device), _dev_as(seq_lens, "seq_lens", i32, device)
+    qp = _dev_as(q, "q", act, device)
     n = seq_lens.numel()
+    qs = q.shape
+    rows = qs[0] if prefill and len(qs) == 3 else n
+    shape = (rows, H_q, d)
+    if qs != shape:
+        _reject(q, "q", act, device, shape)
+    op = _dev_as(out, "out", act, device, shape)
+    kp, vp = _pools(pool, k_pool, v_pool, device)
     ts = block_tables.shape
     if len(ts) != 2 or ts[0] != n:
         raise ValueError(f"block_tables has shape {tuple(ts)}, not ({n}, W)")
-    return qp, kp, vp, tp, ts[1], lp, n, op
+    return qp, rows, kp, vp, tp, ts[1], lp, n, op
 
 
 def pkv_decode_attention_window(pool: Pool, layer: int, q, k_pool, v_pool, block_tables, seq_lens, window: int,
@@ -861,12 +868,12 @@ def pkv_decode_attention_window(pool: Pool, layer: int, q, k_pool, v_pool, block
     """pkv_decode_attention over the last `window` keys of each sequence and its first `n_sink`."""
     L = _lib or _L()
     dev = _current_device()
-    qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out,
-                                                   seq_lens.numel(), dev)
+    qp, _, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, False, dev)
+    ws = _dev(workspace, "workspace")
     if workspace.get_device() != dev:
         _reject(workspace, "workspace", (workspace.dtype,), dev)
-    rc = L.pkv_decode_attention_window(pool.handle, layer, qp, kp, vp, tp, W, lp, n, window, n_sink, scale, op,
-                                       _dev(workspace, "workspace"), workspace.nbytes, _stream_on(stream, dev))
+    rc = L.pkv_decode_attention_window(pool.handle, layer, qp, kp, vp, tp, W, lp, n, min(window, _I32_MAX),
+                                       min(n_sink, _I32_MAX), scale, op, ws, workspace.nbytes, _stream_on(stream, dev))
     if rc:
         _check(rc, "pkv_decode_attention_window")
 
@@ -874,16 +881,18 @@ def pkv_decode_attention_window(pool: Pool, layer: int, q, k_pool, v_pool, block
 def pkv_prefill_attention_window(pool: Pool, layer: int, q, q_offsets, max_q: int, k_pool, v_pool, block_tables,
                                  seq_lens, window: int, n_sink: int, scale: float, out, stream=None) -> None:
     """pkv_prefill_attention in which the query at position p sees its last `window` keys and the
-    sequence's first `n_sink`; rows of q and out past q_offsets[n_seq] are left alone."""
+    sequence's first `n_sink`; rows of q past q_offsets[n_seq] have no
+    effect, rows of out there are left alone."""
     L = _lib or _L()
     dev = _current_device()
-    n_tok = q.shape[0]
-    qp, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, n_tok, dev)
+    qp, n_tok, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, True,
+                                                          dev)
     offs = _dev_as(q_offsets, "q_offsets", _TORCH_TYPES["i32"][1], dev)
     if q_offsets.numel() != n + 1:
         raise ValueError(f"q_offsets has {q_offsets.numel()} entries, not {n + 1}")
-    rc = L.pkv_prefill_attention_window(pool.handle, layer, qp, offs, n_tok, max_q, kp, vp, tp, W, lp, n, window,
-                                        n_sink, scale, op, _stream_on(stream, dev))
+    rc = L.pkv_prefill_attention_window(pool.handle, layer, qp, offs, n_tok, max_q, kp, vp, tp, W, lp, n,
+                                        min(window, _I32_MAX), min(n_sink, _I32_MAX), scale, op,
+                                        _stream_on(stream, dev))
     if rc:
         _check(rc, "pkv_prefill_attention_window")
 

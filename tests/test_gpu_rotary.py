@@ -222,6 +222,9 @@ def test_refusals_of_the_binding():
         (dict(positions=c.positions.long()), TypeError, "positions"),
         (dict(positions=c.positions[:, :-1].contiguous()), ValueError, "positions"),
         (dict(slot_mapping=c.slots[:-1].contiguous()), ValueError, "positions"),
+        (dict(slot_mapping=None), TypeError, "slot_mapping must"),
+        (dict(positions=None), TypeError, "positions must"),
+        (dict(k_new=None), TypeError, "k_new must"),
     ]:
         with pytest.raises(error, match=text):
             c.call(**kw)

@@ -351,6 +351,15 @@ def test_prefill_rows_depend_on_their_own_sequence_alone(dtype, H_q, H_kv):
     assert torch.equal(b.out[:b.offs[-1]], first[:b.offs[-1]])
 
 
+@pytest.mark.parametrize("chunks", [None, [5, 1, 40]])
+def test_windows_past_32_bits_are_every_key(chunks):
+    b = Batch("bf16", [300, 1, 40], 2**31 - 1, 0, chunks)
+    for kw in (dict(window=2**32 + 5), dict(window=2**31), dict(window=3, n_sink=2**32 + 1)):
+        b.out.fill_(math.nan)
+        b.call(**kw)
+        b.check()
+
+
 def test_replayed_graphs_that_share_a_workspace():
     """Every replay counts its split pairs anew: two graphs, replayed in turn with new lengths, queries and workspace bytes."""
     a = Batch("bf16", [3000, 17, 800], 900, 4, H_q=64, H_kv=8)
@@ -446,6 +455,17 @@ def test_refusals():
             with pytest.raises(error, match=text):
                 x.call(**kw)
         assert bool(torch.isnan(x.out).all())
+        for name, text in [("q", "q must"), ("tables", "block_tables must"), ("lens", "seq_lens must"), ("out", "out must")]:
+            for wrong in (None, [1, 2], getattr(x, {"lens": "lens_d"}.get(name, name)).cpu()):
+                with pytest.raises(TypeError, match=text):
+                    x.call(**{name: wrong})
+        shifted = torch.zeros(x.q.numel() + 1, dtype=x.q.dtype, device="cuda")[1:].view(x.q.shape)
+        for name in ("q", "out"):
+            with pytest.raises(pkv.PkvError, match="aligned"):
+                x.call(**{name: shifted})
+    for wrong in (None, b.ws.cpu()):
+        with pytest.raises(TypeError, match="workspace must"):
+            b.call(ws=wrong)
     with pytest.raises(pkv.PkvError, match="workspace"):
         b.call(ws=b.ws[:256])
     with pytest.raises(ValueError, match="q_offsets"):
