@@ -881,8 +881,8 @@ def pkv_decode_attention_window(pool: Pool, layer: int, q, k_pool, v_pool, block
 def pkv_prefill_attention_window(pool: Pool, layer: int, q, q_offsets, max_q: int, k_pool, v_pool, block_tables,
                                  seq_lens, window: int, n_sink: int, scale: float, out, stream=None) -> None:
     """pkv_prefill_attention in which the query at position p sees its last `window` keys and the
-    sequence's first `n_sink`; rows of q past q_offsets[n_seq] have no
-    effect, rows of out there are left alone."""
+    sequence's first `n_sink`; rows of q past q_offsets[n_seq] have no effect, those of out
+    are left alone."""
     L = _lib or _L()
     dev = _current_device()
     qp, n_tok, kp, vp, tp, W, lp, n, op = _attention_args(pool, q, k_pool, v_pool, block_tables, seq_lens, out, True,
