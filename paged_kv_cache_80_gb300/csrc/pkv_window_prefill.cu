@@ -15,7 +15,7 @@
 // them: Q K, softmax, P V of a key tile follow each other, and only the other row tile fills the gaps.
 //   * 16-bit pools: 128-key tiles (N = 128 products keep their shared-memory reads, 8 KB a K = 16 step, in step with the
 //     multiplies).  S of both tiles and O fill TMEM, so S has one buffer; A and B take turns at the tensor cores, (P V,
-//     Q K) of one, then of the other, and P V starts with half of P.  8 x 512 queries, window 4,096: 392 us,
+//     Q K) of one, then of the other, and P V starts with half of P.  8 x 512 queries, window 4,096: 398 us,
 //     0.73 of cuBLAS's rate (567 us for the kernel of the calls without a window, given this mask).  Of a key tile's 3,300
 //     cycles the tensor cores work 2,050.  Measured and not kept: 64-key tiles with two S buffers (445 us: the products of
 //     N = 64 wait for shared memory), issuing without turns (530 us: both tiles' softmaxes run at once, then both
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(WpCfg<KV8, D>::THREADS, 1)
         };
         // The reference maximum of a row moves only when the row's grows by more than 2^8 (until then P and l share the
         // old one), which is rare after the first tile.  E4M3 pools take the exponentials with the old one while the new
-        // maximum is found, and once more if it moves (305 -> 300 us; with 16-bit pools' longer turns it costs 9 %).
+        // maximum is found, and once more if it moves (305 -> 303 us; with 16-bit pools' longer turns it costs 9 %).
         const bool early = KV8 && !__any_sync(0xffffffffu, m == -INFINITY);
         if (early)
 #pragma unroll
